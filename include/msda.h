@@ -544,6 +544,41 @@ msda_status_t sca_backward_full(const void* value, msda_dtype_t vdt,
                                 float* grad_sampling_offsets, float* grad_attention_logits,
                                 float* grad_reference_points_cam, msda_stream_t stream);
 
+/* One gradient tensor of msda_clip_grad_norm. */
+typedef struct {
+    const void* grad;        /* numel values of grad_dtype, read */
+    void* out;               /* numel values of out_dtype, written: the clipped gradient.
+                                out == grad (the same dtype) clips in place; NULL: the
+                                tensor counts in the norm and is not written */
+    int64_t numel;           /* >= 0; pointers of an empty tensor are not looked at */
+    msda_dtype_t grad_dtype; /* MSDA_F32 or MSDA_BF16 */
+    msda_dtype_t out_dtype;
+} msda_grad_t;
+
+/* The global norm of all gradients, and their clipping by it (the pages give
+ * no training step; this follows the backward calls above in one):
+ *   total = grad_scale * sqrt(sum over all tensors and values of g^2)
+ *   out   = g * f,  f = grad_scale * min(1, max_norm / (total + eps))
+ * with f rounded once to fp32 and the product once to out_dtype.  grad_scale
+ * takes a loss scale off (1 where there is none).  The squares are exact and
+ * summed in double in a fixed order: no overflow, no underflow, the same bits
+ * on every run.  A NaN among the gradients makes total and every out NaN; an
+ * infinity makes total infinite and f = 0 (so infinite values become NaN).
+ * max_norm = +infinity only scales (f = grad_scale).
+ *   tensors    [count] HOST array, read during the call, not kept
+ *   total_norm [1] fp32 device, written
+ *   workspace  >= msda_clip_grad_norm_workspace_size(count) bytes, 256-byte
+ *              aligned, contents ignored
+ * max_norm >= 0, eps > 0 and grad_scale > 0 (finite, but max_norm).  Tensors
+ * need the alignment of their type only.  No tensor may be listed twice, and
+ * no out may overlap another tensor's grad or out, nor its own grad but for
+ * out == grad: MSDA_ERR_INVALID_ARG. */
+size_t msda_clip_grad_norm_workspace_size(int32_t count);
+msda_status_t msda_clip_grad_norm(const msda_grad_t* tensors, int32_t count, float max_norm,
+                                  float eps, float grad_scale, void* workspace,
+                                  size_t workspace_bytes, float* total_norm,
+                                  msda_stream_t stream);
+
 /* Fixed text for a status code. */
 const char* msda_status_string(msda_status_t status);
 

@@ -15,6 +15,7 @@ and ``msda_backward`` (``deterministic=True``: the fixed-point variants),
 ``sca_backward_full``,
 ``sca_backward_inputs``, ``tsa_reference_points``, ``tsa_forward``,
 ``tsa_backward``, ``msda_linear`` (with dropout), ``sca_module_forward``,
+``msda_clip_grad_norm``,
 ``msda_workspace_size``, ``sca_compact_workspace_size``; the remaining C
 entry points (workspace sizes, status strings, the no-alloc compaction, the
 GEMM's timeout counter and test switch) are reached through ``lib()``.
@@ -49,6 +50,12 @@ class ScaModuleParams(ctypes.Structure):
                 ("reference_points_cam", _vp), ("bev_mask", _vp), ("value_dtype", ctypes.c_int),
                 ("dropout_p", ctypes.c_float), ("dropout_seed", ctypes.c_uint64),
                 ("camera_embeds", _vp), ("level_embeds", _vp)]
+
+
+class Grad(ctypes.Structure):
+    """msda_grad_t: one gradient tensor of msda_clip_grad_norm."""
+    _fields_ = [("grad", _vp), ("out", _vp), ("numel", ctypes.c_int64),
+                ("grad_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int)]
 
 
 _lib = None
@@ -134,6 +141,11 @@ def lib():
         L.sca_forward_query_major.argtypes = [_vp, st, _i64p, _i64p, _vp, _vp, _vp, _vp, Dims,
                                               _vp, _vp]
         L.sca_forward_query_major.restype = ctypes.c_int
+        L.msda_clip_grad_norm_workspace_size.argtypes = [i32]
+        L.msda_clip_grad_norm_workspace_size.restype = ctypes.c_size_t
+        L.msda_clip_grad_norm.argtypes = [_vp, i32, ctypes.c_float, ctypes.c_float,
+                                          ctypes.c_float, _vp, ctypes.c_size_t, _vp, _vp]
+        L.msda_clip_grad_norm.restype = ctypes.c_int
         L.msda_status_string.argtypes = [ctypes.c_int]
         L.msda_status_string.restype = ctypes.c_char_p
         L.msda_last_error.restype = ctypes.c_char_p
@@ -193,6 +205,21 @@ def _contig(*ts):
     for t in ts:
         if t is not None and not t.is_contiguous():
             raise MsdaError("tensors must be contiguous")
+
+
+def _scope(name, stream, *ts):
+    """The context of a call on the tensors' device: that device current and
+    `stream` (of that device), when given, the current stream, so that what is
+    allocated inside belongs to the stream that the kernels run on."""
+    torch = _torch()
+    dev = ts[0].device
+    if any(t is not None and (not t.is_cuda or t.device != dev) for t in ts):
+        raise MsdaError(f"{name}: the tensors must be on one CUDA device")
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise MsdaError(f"{name}: the stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream)
 
 
 def msda_forward(value, spatial_shapes, level_start_index, sampling_locations,
@@ -683,3 +710,71 @@ def sca_backward_inputs(spatial_shapes, level_start_index, attention_logits, pos
                                      _ptr(g_ref), _stream(stream)),
            "sca_backward_inputs")
     return g_off, g_lg, g_ref
+
+
+_GRAD_T = np.dtype([("grad", np.uintp), ("out", np.uintp), ("numel", np.int64),
+                    ("grad_dtype", np.int32), ("out_dtype", np.int32)])
+
+
+def _same_dense_layout(a, b):
+    """Whether a and b hold one value per element in the same order, without gaps."""
+    torch = _torch()
+    return a.stride() == b.stride() and (
+        a.is_contiguous() or (a.dim() == 4 and a.is_contiguous(memory_format=torch.channels_last))
+        or (a.dim() == 5 and a.is_contiguous(memory_format=torch.channels_last_3d)))
+
+
+def msda_clip_grad_norm(grads, max_norm, eps=1e-6, grad_scale=1.0, out=None, total_norm=None,
+                        workspace=None, stream=None):
+    """The gradients (a list of fp32 or bf16 tensors) scaled by grad_scale and
+    clipped to the global norm max_norm, in place or into `out` (a list of the
+    same shapes, fp32 or bf16) -> total_norm [1] fp32, the norm before the
+    clipping.  Tensors are contiguous, or channels-last (then `out` too)."""
+    torch = _torch()
+    grads = list(grads)
+    n = len(grads)
+    outs = grads if out is None else list(out)
+    if len(outs) != n:
+        raise MsdaError(f"msda_clip_grad_norm: {n} gradients and {len(outs)} outputs")
+    if n == 0 and total_norm is None:
+        raise MsdaError("msda_clip_grad_norm: no gradients, and no total_norm to write")
+    first = grads[0] if n else total_norm
+    index = first.get_device()
+    if index < 0 or any(t.get_device() != index for t in grads):
+        raise MsdaError("msda_clip_grad_norm: the tensors must be on one CUDA device")
+    codes = {torch.float32: MSDA_F32, torch.bfloat16: MSDA_BF16}
+    table = np.empty(n, _GRAD_T)
+    try:
+        table["grad_dtype"] = [codes[t.dtype] for t in grads]
+        table["out_dtype"] = (table["grad_dtype"] if out is None
+                              else [codes[t.dtype] for t in outs])
+    except KeyError as e:
+        raise MsdaError(f"msda_clip_grad_norm: dtype {e.args[0]} is not float32 or bfloat16") \
+            from None
+    table["grad"] = [t.data_ptr() for t in grads]
+    table["numel"] = [t.numel() for t in grads]
+    if out is None:
+        table["out"] = table["grad"]
+        if not all(t.is_contiguous() or _same_dense_layout(t, t) for t in grads):
+            raise MsdaError("msda_clip_grad_norm: a gradient is not dense")
+    else:
+        table["out"] = [t.data_ptr() for t in outs]
+        if any(t.get_device() != index for t in outs):
+            raise MsdaError("msda_clip_grad_norm: the tensors must be on one CUDA device")
+        for g, o in zip(grads, outs):
+            if g.shape != o.shape or not ((g.is_contiguous() and o.is_contiguous())
+                                          or _same_dense_layout(g, o)):
+                raise MsdaError("msda_clip_grad_norm: an output is not laid out as its gradient")
+    with _scope("msda_clip_grad_norm", stream, first, total_norm, workspace):
+        if total_norm is None:
+            total_norm = torch.empty(1, device=first.device, dtype=torch.float32)
+        elif total_norm.dtype != torch.float32 or total_norm.numel() != 1:
+            raise MsdaError("msda_clip_grad_norm: total_norm must be one float32 value")
+        workspace = _workspace(int(lib().msda_clip_grad_norm_workspace_size(n)), first.device,
+                               workspace)
+        _check(lib().msda_clip_grad_norm(ctypes.c_void_p(table.ctypes.data), n, max_norm, eps,
+                                         grad_scale, _ptr(workspace),
+                                         workspace.numel() * workspace.element_size(),
+                                         _ptr(total_norm), _stream(None)),
+               "msda_clip_grad_norm")
+    return total_norm

@@ -798,6 +798,14 @@ extern "C" msda_status_t sca_backward_inputs(const int64_t* spatial_shapes,
 // share this file's per-thread error message).
 namespace msda {
 msda_status_t api_fail(msda_status_t code, const char* message) { return fail(code, "%s", message); }
+msda_status_t api_failf(msda_status_t code, const char* fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_error, sizeof(g_error), fmt, ap);
+    va_end(ap);
+    return code;
+}
 msda_status_t api_ok() { return ok(); }
 msda_status_t api_cuda(cudaError_t e, const char* where) { return cuda_status(e, where); }
 }  // namespace msda

@@ -194,6 +194,7 @@ cudaError_t launch_tsa_backward(const Problem& p, int T, const float* ref, const
 
 // Set the per-thread error message of msda_last_error() and return the code.
 msda_status_t api_fail(msda_status_t code, const char* message);
+msda_status_t api_failf(msda_status_t code, const char* fmt, ...);
 msda_status_t api_ok();
 msda_status_t api_cuda(cudaError_t e, const char* where);
 }  // namespace msda
