@@ -544,6 +544,73 @@ msda_status_t sca_backward_full(const void* value, msda_dtype_t vdt,
                                 float* grad_sampling_offsets, float* grad_attention_logits,
                                 float* grad_reference_points_cam, msda_stream_t stream);
 
+/* Sizes of the group norm over packed multi-level rows. */
+typedef struct {
+    int32_t B;  /* items: batch items, or batch items times cameras */
+    int32_t Nv; /* rows per item, >= every level_start_index[l] + H_l * W_l */
+    int32_t C;  /* channels of a row, a multiple of 8, at most MSDA_NORM_MAX_CHANNELS */
+    int32_t L;  /* levels, 1 .. MSDA_MAX_LEVELS; they may not share rows */
+    int32_t G;  /* groups, divides C: group g holds the channels [g C / G, (g + 1) C / G) */
+} msda_norm_dims_t;
+
+#define MSDA_NORM_MAX_CHANNELS 2048
+
+typedef enum {
+    MSDA_ACT_NONE = 0, /* z */
+    MSDA_ACT_RELU = 1, /* max(z, 0); a NaN stays */
+    MSDA_ACT_SILU = 2  /* z / (1 + exp(-z)) */
+} msda_activation_t;
+
+/* Group norm of every level of channels-last rows, with its activation: the
+ * step between a pyramid's projections and the value rows that MSDA reads
+ * (the pages take normalised features as given).  Per item b, level l and
+ * group g, over all the level's rows and the group's channels:
+ *   mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps)
+ *   z  = gamma[l, c] (x - mu) r + beta[l, c],   y = act(z)
+ * The layout is the value's: pixel (y, x) of level l is row
+ * level_start_index[l] + y * W_l + x; rows of no level get 0.
+ *   x           [B, Nv, C]   fp32 or bf16 (x_dtype)
+ *   gamma, beta [L, C]       fp32; NULL: 1 and 0
+ *   y           [B, Nv, C]   fp32 or bf16 (y_dtype), written; not x
+ *   mean, rstd  [B, L, G]    fp32, written; for the backward (NULL: not wanted)
+ * The statistics are accumulated relative to values of the data and merged in
+ * double (no cancellation when the mean is far from zero), and the same on
+ * every run.  eps: finite, > 0.  x, y, gamma and beta 16-byte aligned;
+ * workspace >= msda_group_norm_workspace_size(d) bytes, 256-byte aligned,
+ * contents ignored. */
+size_t msda_group_norm_workspace_size(msda_norm_dims_t d);
+msda_status_t msda_group_norm(const void* x, msda_dtype_t x_dtype, const int64_t* spatial_shapes,
+                              const int64_t* level_start_index, msda_norm_dims_t d,
+                              const float* gamma, const float* beta, float eps,
+                              msda_activation_t act, msda_dtype_t y_dtype, void* y, float* mean,
+                              float* rstd, void* workspace, size_t workspace_bytes,
+                              msda_stream_t stream);
+
+/* The derivative of msda_group_norm.  With xh = (x - mean) rstd, z as above
+ * and dz = grad_y act'(z) (relu: 1 where z > 0, z taken exactly at the
+ * border; 0 elsewhere):
+ *   grad_gamma[l, c] = sum over b and rows of dz xh
+ *   grad_beta[l, c]  = sum over b and rows of dz
+ *   grad_x = rstd (t - mean(t) - xh mean(t xh)),  t = gamma dz,
+ * the means over the group's rows and channels.  Deterministic (no atomics).
+ *   x, gamma, beta, act as in the forward; mean, rstd [B, L, G] from it
+ *   grad_y     [B, Nv, C] fp32 or bf16 (gy_dtype); rows of no level not read
+ *   grad_x     [B, Nv, C] fp32 or bf16 (gx_dtype), written, 0 in rows of no
+ *              level; neither x nor grad_y
+ *   grad_gamma, grad_beta [L, C] fp32, written (NULL: not wanted)
+ * Alignment and workspace as in the forward, with
+ * msda_group_norm_backward_workspace_size(d). */
+size_t msda_group_norm_backward_workspace_size(msda_norm_dims_t d);
+msda_status_t msda_group_norm_backward(const void* x, msda_dtype_t x_dtype,
+                                       const int64_t* spatial_shapes,
+                                       const int64_t* level_start_index, msda_norm_dims_t d,
+                                       const float* gamma, const float* beta, const float* mean,
+                                       const float* rstd, msda_activation_t act,
+                                       const void* grad_y, msda_dtype_t gy_dtype,
+                                       msda_dtype_t gx_dtype, void* grad_x, float* grad_gamma,
+                                       float* grad_beta, void* workspace, size_t workspace_bytes,
+                                       msda_stream_t stream);
+
 /* One gradient tensor of msda_clip_grad_norm. */
 typedef struct {
     const void* grad;        /* numel values of grad_dtype, read */

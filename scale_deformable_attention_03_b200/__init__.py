@@ -15,12 +15,13 @@ and ``msda_backward`` (``deterministic=True``: the fixed-point variants),
 ``sca_backward_full``,
 ``sca_backward_inputs``, ``tsa_reference_points``, ``tsa_forward``,
 ``tsa_backward``, ``msda_linear`` (with dropout), ``sca_module_forward``,
-``msda_clip_grad_norm``,
+``msda_group_norm``, ``msda_group_norm_backward``, ``msda_clip_grad_norm``,
 ``msda_workspace_size``, ``sca_compact_workspace_size``; the remaining C
 entry points (workspace sizes, status strings, the no-alloc compaction, the
 GEMM's timeout counter and test switch) are reached through ``lib()``.
 """
 import ctypes
+import operator
 import os
 
 import numpy as np
@@ -50,6 +51,11 @@ class ScaModuleParams(ctypes.Structure):
                 ("reference_points_cam", _vp), ("bev_mask", _vp), ("value_dtype", ctypes.c_int),
                 ("dropout_p", ctypes.c_float), ("dropout_seed", ctypes.c_uint64),
                 ("camera_embeds", _vp), ("level_embeds", _vp)]
+
+
+class NormDims(ctypes.Structure):
+    """msda_norm_dims_t."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "Nv", "C", "L", "G")]
 
 
 class Grad(ctypes.Structure):
@@ -141,6 +147,17 @@ def lib():
         L.sca_forward_query_major.argtypes = [_vp, st, _i64p, _i64p, _vp, _vp, _vp, _vp, Dims,
                                               _vp, _vp]
         L.sca_forward_query_major.restype = ctypes.c_int
+        L.msda_group_norm_workspace_size.argtypes = [NormDims]
+        L.msda_group_norm_workspace_size.restype = ctypes.c_size_t
+        L.msda_group_norm.argtypes = [_vp, st, _i64p, _i64p, NormDims, _vp, _vp, ctypes.c_float,
+                                      st, st, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+        L.msda_group_norm.restype = ctypes.c_int
+        L.msda_group_norm_backward_workspace_size.argtypes = [NormDims]
+        L.msda_group_norm_backward_workspace_size.restype = ctypes.c_size_t
+        L.msda_group_norm_backward.argtypes = [_vp, st, _i64p, _i64p, NormDims, _vp, _vp, _vp,
+                                               _vp, st, _vp, st, st, _vp, _vp, _vp, _vp,
+                                               ctypes.c_size_t, _vp]
+        L.msda_group_norm_backward.restype = ctypes.c_int
         L.msda_clip_grad_norm_workspace_size.argtypes = [i32]
         L.msda_clip_grad_norm_workspace_size.restype = ctypes.c_size_t
         L.msda_clip_grad_norm.argtypes = [_vp, i32, ctypes.c_float, ctypes.c_float,
@@ -729,7 +746,8 @@ def msda_clip_grad_norm(grads, max_norm, eps=1e-6, grad_scale=1.0, out=None, tot
     """The gradients (a list of fp32 or bf16 tensors) scaled by grad_scale and
     clipped to the global norm max_norm, in place or into `out` (a list of the
     same shapes, fp32 or bf16) -> total_norm [1] fp32, the norm before the
-    clipping.  Tensors are contiguous, or channels-last (then `out` too)."""
+    clipping.  Tensors are contiguous, or
+    channels-last together with their outputs."""
     torch = _torch()
     grads = list(grads)
     n = len(grads)
@@ -738,33 +756,30 @@ def msda_clip_grad_norm(grads, max_norm, eps=1e-6, grad_scale=1.0, out=None, tot
         raise MsdaError(f"msda_clip_grad_norm: {n} gradients and {len(outs)} outputs")
     if n == 0 and total_norm is None:
         raise MsdaError("msda_clip_grad_norm: no gradients, and no total_norm to write")
-    first = grads[0] if n else total_norm
-    index = first.get_device()
-    if index < 0 or any(t.get_device() != index for t in grads):
+    # one pass over the list per attribute, each a C-level map: of a list of
+    # hundreds these lines are most of the call's host time
+    every = grads if out is None else grads + outs
+    Tensor = torch.Tensor
+    first = every[0] if n else total_norm
+    if first.get_device() < 0 or len(set(map(Tensor.get_device, every))) > 1:
         raise MsdaError("msda_clip_grad_norm: the tensors must be on one CUDA device")
+    dtypes = list(map(operator.attrgetter("dtype"), every))
     codes = {torch.float32: MSDA_F32, torch.bfloat16: MSDA_BF16}
+    if not codes.keys() >= set(dtypes):
+        raise MsdaError("msda_clip_grad_norm: a tensor is neither float32 nor bfloat16")
+    sizes = list(map(Tensor.numel, every))
+    if not all(map(Tensor.is_contiguous, every)):
+        if not all(g.shape == o.shape and _same_dense_layout(g, o) for g, o in zip(grads, outs)):
+            raise MsdaError("msda_clip_grad_norm: a tensor is not dense, or an output is not "
+                            "laid out as its gradient")
+    elif out is not None and sizes[:n] != sizes[n:]:
+        raise MsdaError("msda_clip_grad_norm: an output has another size than its gradient")
+    pointers = list(map(Tensor.data_ptr, every))
+    kinds = list(map(codes.get, dtypes))
     table = np.empty(n, _GRAD_T)
-    try:
-        table["grad_dtype"] = [codes[t.dtype] for t in grads]
-        table["out_dtype"] = (table["grad_dtype"] if out is None
-                              else [codes[t.dtype] for t in outs])
-    except KeyError as e:
-        raise MsdaError(f"msda_clip_grad_norm: dtype {e.args[0]} is not float32 or bfloat16") \
-            from None
-    table["grad"] = [t.data_ptr() for t in grads]
-    table["numel"] = [t.numel() for t in grads]
-    if out is None:
-        table["out"] = table["grad"]
-        if not all(t.is_contiguous() or _same_dense_layout(t, t) for t in grads):
-            raise MsdaError("msda_clip_grad_norm: a gradient is not dense")
-    else:
-        table["out"] = [t.data_ptr() for t in outs]
-        if any(t.get_device() != index for t in outs):
-            raise MsdaError("msda_clip_grad_norm: the tensors must be on one CUDA device")
-        for g, o in zip(grads, outs):
-            if g.shape != o.shape or not ((g.is_contiguous() and o.is_contiguous())
-                                          or _same_dense_layout(g, o)):
-                raise MsdaError("msda_clip_grad_norm: an output is not laid out as its gradient")
+    table["grad"], table["out"] = pointers[:n], pointers[-n:] if n else []
+    table["numel"] = sizes[:n]
+    table["grad_dtype"], table["out_dtype"] = kinds[:n], kinds[-n:] if n else []
     with _scope("msda_clip_grad_norm", stream, first, total_norm, workspace):
         if total_norm is None:
             total_norm = torch.empty(1, device=first.device, dtype=torch.float32)
@@ -778,3 +793,108 @@ def msda_clip_grad_norm(grads, max_norm, eps=1e-6, grad_scale=1.0, out=None, tot
                                          _ptr(total_norm), _stream(None)),
                "msda_clip_grad_norm")
     return total_norm
+
+
+_ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2}
+
+
+def _arg(name, t, shape, dtypes, what):
+    """An argument's shape, dtype and layout; None passes."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape):
+        raise MsdaError(f"{name}: {what} has the shape {list(t.shape)}, not {list(shape)}")
+    if t.dtype not in dtypes:
+        raise MsdaError(f"{name}: {what} is {t.dtype}")
+    if not t.is_contiguous():
+        raise MsdaError(f"{name}: {what} must be contiguous")
+
+
+def _out(name, t, shape, dtypes, what, device):
+    """An output: the given tensor, checked, or a new one of dtypes[0]."""
+    if t is None:
+        return _torch().empty(shape, device=device, dtype=dtypes[0])
+    _arg(name, t, shape, dtypes, what)
+    return t
+
+
+def _norm_args(name, x, spatial_shapes, level_start_index, num_groups, gamma, beta, activation):
+    torch = _torch()
+    f32, data = (torch.float32,), (torch.float32, torch.bfloat16)
+    if x.dim() < 2:
+        raise MsdaError(f"{name}: x must be [..., Nv, C]")
+    _arg(name, x, x.shape, data, "x")
+    if activation not in _ACTIVATIONS:
+        raise MsdaError(f"{name}: activation {activation!r} is not none, relu or silu")
+    shapes, starts = _levels(spatial_shapes, level_start_index)
+    if len(starts) != len(shapes):
+        raise MsdaError(f"{name}: {len(shapes)} levels and {len(starts)} starts")
+    Nv, C, L, G = x.shape[-2], x.shape[-1], len(shapes), int(num_groups)
+    _arg(name, gamma, (L, C), f32, "gamma")
+    _arg(name, beta, (L, C), f32, "beta")
+    B = 1
+    for s in x.shape[:-2]:
+        B *= s
+    return shapes, starts, NormDims(B, Nv, C, L, G)
+
+
+def msda_group_norm(x, spatial_shapes, level_start_index, num_groups, gamma=None, beta=None,
+                    eps=1e-5, activation="none", out_dtype=None, out=None, mean=None, rstd=None,
+                    workspace=None, stream=None):
+    """Group norm and activation (none, relu, silu) of every level of the
+    channels-last rows x [..., Nv, C] (fp32 or bf16), gamma and beta [L, C]
+    fp32 -> (y [..., Nv, C] of out_dtype, by default x's; mean and rstd
+    [..., L, num_groups] fp32, for the backward).  Rows of no level get 0."""
+    torch = _torch()
+    name = "msda_group_norm"
+    shapes, starts, d = _norm_args(name, x, spatial_shapes, level_start_index, num_groups, gamma,
+                                   beta, activation)
+    f32, data = (torch.float32,), (torch.float32, torch.bfloat16)
+    small = tuple(x.shape[:-2]) + (d.L, d.G)
+    with _scope(name, stream, x, gamma, beta, out, mean, rstd, workspace):
+        y = _out(name, out, x.shape, data if out is not None else (out_dtype or x.dtype,), "out",
+                 x.device)
+        if out_dtype is not None and y.dtype != out_dtype:
+            raise MsdaError(f"{name}: out is {y.dtype}, not {out_dtype}")
+        mean = _out(name, mean, small, f32, "mean", x.device)
+        rstd = _out(name, rstd, small, f32, "rstd", x.device)
+        workspace = _workspace(int(lib().msda_group_norm_workspace_size(d)), x.device, workspace)
+        _check(lib().msda_group_norm(_ptr(x), _vdt(x), shapes.ctypes.data_as(_i64p),
+                                     starts.ctypes.data_as(_i64p), d, _ptr(gamma), _ptr(beta),
+                                     eps, _ACTIVATIONS[activation], _vdt(y), _ptr(y), _ptr(mean),
+                                     _ptr(rstd), _ptr(workspace), workspace.numel(),
+                                     _stream(None)), name)
+    return y, mean, rstd
+
+
+def msda_group_norm_backward(x, spatial_shapes, level_start_index, num_groups, mean, rstd,
+                             grad_out, gamma=None, beta=None, activation="none", out_dtype=None,
+                             out=None, workspace=None, stream=None):
+    """-> (grad_x [..., Nv, C] of out_dtype, by default x's; grad_gamma and
+    grad_beta [L, C] fp32); `out` may supply the three tensors.  mean and rstd
+    come from msda_group_norm."""
+    torch = _torch()
+    name = "msda_group_norm_backward"
+    shapes, starts, d = _norm_args(name, x, spatial_shapes, level_start_index, num_groups, gamma,
+                                   beta, activation)
+    f32, data = (torch.float32,), (torch.float32, torch.bfloat16)
+    small = tuple(x.shape[:-2]) + (d.L, d.G)
+    _arg(name, mean, small, f32, "mean")
+    _arg(name, rstd, small, f32, "rstd")
+    _arg(name, grad_out, x.shape, data, "grad_out")
+    gx, gg, gb = out if out is not None else (None, None, None)
+    with _scope(name, stream, x, gamma, beta, mean, rstd, grad_out, gx, gg, gb, workspace):
+        gx = _out(name, gx, x.shape, data if gx is not None else (out_dtype or x.dtype,), "grad_x",
+                  x.device)
+        if out_dtype is not None and gx.dtype != out_dtype:
+            raise MsdaError(f"{name}: grad_x is {gx.dtype}, not {out_dtype}")
+        gg = _out(name, gg, (d.L, d.C), f32, "grad_gamma", x.device)
+        gb = _out(name, gb, (d.L, d.C), f32, "grad_beta", x.device)
+        workspace = _workspace(int(lib().msda_group_norm_backward_workspace_size(d)), x.device,
+                               workspace)
+        _check(lib().msda_group_norm_backward(
+            _ptr(x), _vdt(x), shapes.ctypes.data_as(_i64p), starts.ctypes.data_as(_i64p), d,
+            _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd), _ACTIVATIONS[activation],
+            _ptr(grad_out), _vdt(grad_out), _vdt(gx), _ptr(gx), _ptr(gg), _ptr(gb),
+            _ptr(workspace), workspace.numel(), _stream(None)), name)
+    return gx, gg, gb

@@ -72,3 +72,94 @@ def test_clip_rejects_bad_tensors(L, tensors, fragment):
 def test_clip_workspace_grows_with_the_table(L):
     f = L.msda_clip_grad_norm_workspace_size
     assert f(0) == f(960) > 0 and f(961) == 2 * f(960)
+
+
+def _tables(shapes=((3, 4), (2, 2)), starts=None):
+    s = np.asarray(shapes, dtype=np.int64).reshape(-1, 2)
+    st = (np.concatenate([[0], np.cumsum(s[:, 0] * s[:, 1])[:-1]]) if starts is None
+          else np.asarray(starts)).astype(np.int64)
+    p = ctypes.POINTER(ctypes.c_int64)
+    return s, st, s.ctypes.data_as(p), st.ctypes.data_as(p)
+
+
+NORM = dict(d=(2, 16, 32, 2, 4), shapes=((3, 4), (2, 2)), starts=None, x=FAKE, xt=0, gamma=None,
+            beta=None, eps=1e-5, act=0, yt=0, y=FAKE + (1 << 30), ws=FAKE + (1 << 31), ws_bytes=None)
+
+
+def _norm(L, **kw):
+    a = dict(NORM, **kw)
+    keep = _tables(a["shapes"], a["starts"])
+    d = msda.NormDims(*a["d"])
+    n = L.msda_group_norm_workspace_size(d) if a["ws_bytes"] is None else a["ws_bytes"]
+    return L.msda_group_norm(a["x"], a["xt"], keep[2], keep[3], d, a["gamma"], a["beta"], a["eps"],
+                             a["act"], a["yt"], a["y"], None, None, a["ws"], n, None)
+
+
+def _norm_back(L, gx=FAKE + (1 << 30), gy=FAKE + (1 << 29), gxt=0, gyt=0, mean=FAKE, **kw):
+    a = dict(NORM, **kw)
+    keep = _tables(a["shapes"], a["starts"])
+    d = msda.NormDims(*a["d"])
+    n = L.msda_group_norm_backward_workspace_size(d) if a["ws_bytes"] is None else a["ws_bytes"]
+    return L.msda_group_norm_backward(a["x"], a["xt"], keep[2], keep[3], d, a["gamma"], a["beta"],
+                                      mean, FAKE, a["act"], gy, gyt, gxt, gx, None, None, a["ws"], n,
+                                      None)
+
+
+NORM_BAD = [
+    (dict(d=(-1, 16, 32, 2, 4)), INVALID, "B (-1)"),
+    (dict(d=(2, 0, 32, 2, 4)), INVALID, "Nv (0)"),
+    (dict(d=(2, 16, 36, 2, 4)), UNSUPPORTED, "C = 36"),
+    (dict(d=(2, 16, 2056, 2, 4)), UNSUPPORTED, "C = 2056"),
+    (dict(d=(2, 16, 0, 2, 4)), UNSUPPORTED, "C = 0"),
+    (dict(d=(2, 16, 32, 0, 4)), UNSUPPORTED, "L = 0"),
+    (dict(d=(2, 16, 32, 9, 4)), UNSUPPORTED, "L = 9"),
+    (dict(d=(2, 16, 32, 2, 0)), INVALID, "G = 0"),
+    (dict(d=(2, 16, 32, 2, 3)), INVALID, "G = 3"),
+    (dict(d=(2, 15, 32, 2, 4)), INVALID, "does not fit"),
+    (dict(starts=(0, -1)), INVALID, "does not fit"),
+    (dict(starts=(0, 11)), INVALID, "shares rows"),
+    (dict(starts=(3, 0)), INVALID, "shares rows"),
+    (dict(shapes=((3, 4), (0, 2)), starts=(0, 12)), INVALID, "shape"),
+    (dict(d=(2 ** 30, 2 ** 20, 2048, 2, 4)), UNSUPPORTED, "too many rows"),
+    (dict(x=0), INVALID, "x is null"),
+    (dict(x=FAKE + 8), INVALID, "x must be 16-byte"),
+    (dict(xt=5), INVALID, "x_dtype"),
+    (dict(gamma=FAKE + 4), INVALID, "gamma"),
+    (dict(beta=FAKE + 4), INVALID, "beta"),
+    (dict(act=3), INVALID, "activation"),
+    (dict(ws=None), WORKSPACE, "workspace"),
+    (dict(ws=FAKE + 128), WORKSPACE, "workspace"),
+    (dict(ws_bytes=64), WORKSPACE, "workspace"),
+]
+
+
+@pytest.mark.parametrize("kw,code,fragment", NORM_BAD + [
+    (dict(yt=2), INVALID, "y_dtype"),
+    (dict(y=None), INVALID, "y is null"),
+    (dict(y=FAKE), INVALID, "overlaps"),
+    (dict(y=FAKE + 2 * 16 * 32 * 4 - 16), INVALID, "overlaps"),
+    (dict(eps=0.0), INVALID, "eps"),
+    (dict(eps=math.nan), INVALID, "eps"),
+])
+def test_group_norm_rejects(L, kw, code, fragment):
+    assert _norm(L, **kw) == code
+    assert fragment in L.msda_last_error().decode()
+
+
+@pytest.mark.parametrize("kw,code,fragment", NORM_BAD + [
+    (dict(gxt=2), INVALID, "gx_dtype"),
+    (dict(gyt=2), INVALID, "gy_dtype"),
+    (dict(gx=None), INVALID, "grad_x is null"),
+    (dict(gy=None), INVALID, "grad_y is null"),
+    (dict(mean=None), INVALID, "mean is null"),
+    (dict(gx=FAKE), INVALID, "overlaps"),
+    (dict(gx=FAKE + (1 << 29)), INVALID, "overlaps"),
+])
+def test_group_norm_backward_rejects(L, kw, code, fragment):
+    assert _norm_back(L, **kw) == code
+    assert fragment in L.msda_last_error().decode()
+
+
+def test_group_norm_of_no_items(L):
+    assert _norm(L, d=(0, 16, 32, 2, 4), x=0, y=0, ws=0) == OK
+    assert _norm_back(L, d=(0, 16, 32, 2, 4), x=0, gx=0, gy=0, mean=0, ws=0) == OK
