@@ -611,6 +611,70 @@ msda_status_t msda_group_norm_backward(const void* x, msda_dtype_t x_dtype,
                                        float* grad_beta, void* workspace, size_t workspace_bytes,
                                        msda_stream_t stream);
 
+/* Inputs of the attention among object queries. */
+typedef struct {
+    const void* q;         /* [B, Nq, H, 32] bf16 */
+    const void* k;         /* [B, Nk, H, 32] bf16 */
+    const void* v;         /* [B, Nk, H, 32] bf16 */
+    int64_t q_stride;      /* values from one row (all heads of a query) to the next: */
+    int64_t k_stride;      /* at least H * 32, a multiple of 8; the items follow one */
+    int64_t v_stride;      /* another, Nq or Nk rows apart */
+    const float* q_points; /* [B, Nq, 2] fp32, or NULL (then k_points and tau are NULL) */
+    const float* k_points; /* [B, Nk, 2] fp32 */
+    const float* tau;      /* [B, Nq, H] fp32 */
+    const int32_t* q_group; /* [B, Nq], or NULL (then k_group is NULL) */
+    const int32_t* k_group; /* [B, Nk] */
+    float scale;           /* of the products, usually 32^-1/2; finite */
+    int32_t B, Nq, Nk, H;
+} msda_attention_t;
+
+/* Attention among object queries, whose scores fall with the distance of
+ * their reference points: the decoder's other attention, beside the MSDA that
+ * reads the maps (the pages give the generic softmax(Q K^T / sqrt(d)) V of
+ * [TS] 二; the bias and the groups are this library's).
+ *   s_ij = scale q_i . k_j - tau[b, i, h] |q_points_i - k_points_j|
+ *   query i sees key j when q_group_i >= 0 and k_group_j is 0 or q_group_i:
+ *     keys of group 0 are everybody's (a shared prefix), other groups see
+ *     themselves and those (documents, groups of noised queries), and rows
+ *     with a negative group are padding, which neither sees nor is seen
+ *   lse_i = log sum over seen j of exp(s_ij),
+ *   out_i = sum over seen j of exp(s_ij - lse_i) v_j
+ * A query that sees nothing gets out = 0 and lse = -infinity.  What rows of
+ * padding hold, NaN included, reaches no other row; a key that is seen by some
+ * query has to be finite.  Without points there is no bias, without groups
+ * everybody sees everything.
+ *   out [B, Nq, H * 32] bf16, written
+ *   lse [B, H, Nq]      fp32, written; for the backward (NULL: not wanted)
+ * The products are exact and accumulate in fp32, softmax and sums are fp32;
+ * the weights are rounded to bf16 for their product with v.  q, k, v and out
+ * 16-byte aligned, points 8-byte; workspace >=
+ * msda_query_attention_workspace_size(p) bytes (which looks at B, Nq, Nk and
+ * H), 256-byte aligned, contents ignored. */
+size_t msda_query_attention_workspace_size(const msda_attention_t* p);
+msda_status_t msda_query_attention(const msda_attention_t* p, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes,
+                                   msda_stream_t stream);
+
+/* The derivative of msda_query_attention.  With p_ij = exp(s_ij - lse_i),
+ * dp_ij = grad_out_i . v_j and ds_ij = p_ij (dp_ij - sum_j p_ij dp_ij):
+ *   grad_v_j = sum_i p_ij grad_out_i,  grad_q_i = scale sum_j ds_ij k_j,
+ *   grad_k_j = scale sum_i ds_ij q_i,  grad_tau_i = -sum_j ds_ij |distance|
+ * The points are constants (reference points are passed on detached).  Rows
+ * that see or are seen by nothing get 0.  Deterministic (no atomics).
+ *   lse      [B, H, Nq] fp32, from the forward of the same inputs
+ *   grad_out [B, Nq, H * 32] bf16
+ *   grad_q [B, Nq, H, 32], grad_k and grad_v [B, Nk, H, 32] bf16, contiguous,
+ *   written; grad_tau [B, Nq, H] fp32, written (NULL where p->tau is)
+ * p and ds are rounded to bf16 for the products with grad_out, k and q; the
+ * sum over j of p dp is formed in fp32 from the unrounded values.  Alignment
+ * and workspace as in the forward, with
+ * msda_query_attention_backward_workspace_size(p). */
+size_t msda_query_attention_backward_workspace_size(const msda_attention_t* p);
+msda_status_t msda_query_attention_backward(const msda_attention_t* p, const float* lse,
+                                            const void* grad_out, void* grad_q, void* grad_k,
+                                            void* grad_v, float* grad_tau, void* workspace,
+                                            size_t workspace_bytes, msda_stream_t stream);
+
 /* One gradient tensor of msda_clip_grad_norm. */
 typedef struct {
     const void* grad;        /* numel values of grad_dtype, read */

@@ -15,7 +15,8 @@ and ``msda_backward`` (``deterministic=True``: the fixed-point variants),
 ``sca_backward_full``,
 ``sca_backward_inputs``, ``tsa_reference_points``, ``tsa_forward``,
 ``tsa_backward``, ``msda_linear`` (with dropout), ``sca_module_forward``,
-``msda_group_norm``, ``msda_group_norm_backward``, ``msda_clip_grad_norm``,
+``msda_group_norm``, ``msda_group_norm_backward``, ``msda_query_attention``,
+``msda_query_attention_backward``, ``msda_clip_grad_norm``,
 ``msda_workspace_size``, ``sca_compact_workspace_size``; the remaining C
 entry points (workspace sizes, status strings, the no-alloc compaction, the
 GEMM's timeout counter and test switch) are reached through ``lib()``.
@@ -56,6 +57,15 @@ class ScaModuleParams(ctypes.Structure):
 class NormDims(ctypes.Structure):
     """msda_norm_dims_t."""
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "Nv", "C", "L", "G")]
+
+
+class Attention(ctypes.Structure):
+    """msda_attention_t: the inputs of msda_query_attention."""
+    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("q_points", _vp),
+                ("k_points", _vp), ("tau", _vp), ("q_group", _vp), ("k_group", _vp),
+                ("scale", ctypes.c_float), ("B", ctypes.c_int32), ("Nq", ctypes.c_int32),
+                ("Nk", ctypes.c_int32), ("H", ctypes.c_int32)]
 
 
 class Grad(ctypes.Structure):
@@ -158,6 +168,16 @@ def lib():
                                                _vp, st, _vp, st, st, _vp, _vp, _vp, _vp,
                                                ctypes.c_size_t, _vp]
         L.msda_group_norm_backward.restype = ctypes.c_int
+        ap = ctypes.POINTER(Attention)
+        L.msda_query_attention_workspace_size.argtypes = [ap]
+        L.msda_query_attention_workspace_size.restype = ctypes.c_size_t
+        L.msda_query_attention.argtypes = [ap, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+        L.msda_query_attention.restype = ctypes.c_int
+        L.msda_query_attention_backward_workspace_size.argtypes = [ap]
+        L.msda_query_attention_backward_workspace_size.restype = ctypes.c_size_t
+        L.msda_query_attention_backward.argtypes = [ap, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                                    ctypes.c_size_t, _vp]
+        L.msda_query_attention_backward.restype = ctypes.c_int
         L.msda_clip_grad_norm_workspace_size.argtypes = [i32]
         L.msda_clip_grad_norm_workspace_size.restype = ctypes.c_size_t
         L.msda_clip_grad_norm.argtypes = [_vp, i32, ctypes.c_float, ctypes.c_float,
@@ -898,3 +918,93 @@ def msda_group_norm_backward(x, spatial_shapes, level_start_index, num_groups, m
             _ptr(grad_out), _vdt(grad_out), _vdt(gx), _ptr(gx), _ptr(gg), _ptr(gb),
             _ptr(workspace), workspace.numel(), _stream(None)), name)
     return gx, gg, gb
+
+
+def _rows_stride(name, t, what):
+    """Values between the rows of a [B, N, H, 32] tensor whose rows are dense
+    and whose items follow one another, such as a slice of a joint projection."""
+    torch = _torch()
+    if t.dim() != 4 or t.shape[3] != HEAD_DIM:
+        raise MsdaError(f"{name}: {what} must be [B, N, H, {HEAD_DIM}]")
+    if t.dtype != torch.bfloat16:
+        raise MsdaError(f"{name}: {what} is {t.dtype}, not bfloat16")
+    B, N, H, _ = t.shape
+    sb, sn, sh, sd = t.stride()
+    row = sn if N > 1 else sb if B > 1 else H * HEAD_DIM
+    if t.numel() and (sd != 1 or (H > 1 and sh != HEAD_DIM) or (B > 1 and sb != N * row)):
+        raise MsdaError(f"{name}: the rows of {what} must be dense and evenly spaced")
+    return row
+
+
+def _attention_args(name, q, k, v, q_points, k_points, tau, q_group, k_group, scale):
+    torch = _torch()
+    strides = [_rows_stride(name, t, w) for t, w in ((q, "q"), (k, "k"), (v, "v"))]
+    (B, Nq, H, _), Nk = q.shape, k.shape[1]
+    if k.shape != (B, Nk, H, HEAD_DIM) or v.shape != k.shape:
+        raise MsdaError(f"{name}: q, k and v are {list(q.shape)}, {list(k.shape)}, {list(v.shape)}")
+    f32, i32 = (torch.float32,), (torch.int32,)
+    _arg(name, q_points, (B, Nq, 2), f32, "q_points")
+    _arg(name, k_points, (B, Nk, 2), f32, "k_points")
+    _arg(name, tau, (B, Nq, H), f32, "tau")
+    _arg(name, q_group, (B, Nq), i32, "q_group")
+    _arg(name, k_group, (B, Nk), i32, "k_group")
+    if len({t is None for t in (q_points, k_points, tau)}) > 1:
+        raise MsdaError(f"{name}: q_points, k_points and tau go together")
+    if (q_group is None) != (k_group is None):
+        raise MsdaError(f"{name}: q_group and k_group go together")
+    return Attention(_ptr(q), _ptr(k), _ptr(v), *strides, _ptr(q_points), _ptr(k_points),
+                     _ptr(tau), _ptr(q_group), _ptr(k_group),
+                     HEAD_DIM ** -0.5 if scale is None else scale, B, Nq, Nk, H)
+
+
+def msda_query_attention(q, k, v, q_points=None, k_points=None, tau=None, q_group=None,
+                         k_group=None, scale=None, out=None, lse=None, workspace=None,
+                         stream=None):
+    """Attention of the queries q [B, Nq, H, 32] to k and v [B, Nk, H, 32]
+    (bf16; rows may be slices of a wider projection), the scores lowered by
+    tau [B, Nq, H] times the distance of q_points [B, Nq, 2] and k_points
+    [B, Nk, 2] (fp32), a query seeing the keys of its own group and of group 0
+    (q_group [B, Nq], k_group [B, Nk] int32; negative: padding); scale is
+    32^-1/2 by default -> (out [B, Nq, H * 32] bf16, lse [B, H, Nq] fp32)."""
+    torch = _torch()
+    name = "msda_query_attention"
+    p = _attention_args(name, q, k, v, q_points, k_points, tau, q_group, k_group, scale)
+    with _scope(name, stream, q, k, v, q_points, k_points, tau, q_group, k_group, out, lse,
+                workspace):
+        out = _out(name, out, (p.B, p.Nq, p.H * HEAD_DIM), (torch.bfloat16,), "out", q.device)
+        lse = _out(name, lse, (p.B, p.H, p.Nq), (torch.float32,), "lse", q.device)
+        need = int(lib().msda_query_attention_workspace_size(p))
+        if need:
+            workspace = _workspace(need, q.device, workspace)
+        _check(lib().msda_query_attention(p, _ptr(out), _ptr(lse), _ptr(workspace),
+                                          workspace.numel() if workspace is not None else 0,
+                                          _stream(None)), name)
+    return out, lse
+
+
+def msda_query_attention_backward(q, k, v, lse, grad_out, q_points=None, k_points=None, tau=None,
+                                  q_group=None, k_group=None, scale=None, out=None,
+                                  workspace=None, stream=None):
+    """-> (grad_q [B, Nq, H, 32], grad_k and grad_v [B, Nk, H, 32] bf16,
+    grad_tau [B, Nq, H] fp32 or None without tau); lse comes from the forward
+    of the same inputs, grad_out [B, Nq, H * 32] is bf16, `out` may supply the
+    gradients.  The points get none."""
+    torch = _torch()
+    name = "msda_query_attention_backward"
+    p = _attention_args(name, q, k, v, q_points, k_points, tau, q_group, k_group, scale)
+    b16, f32 = (torch.bfloat16,), (torch.float32,)
+    _arg(name, lse, (p.B, p.H, p.Nq), f32, "lse")
+    _arg(name, grad_out, (p.B, p.Nq, p.H * HEAD_DIM), b16, "grad_out")
+    gq, gk, gv, gt = out if out is not None else (None,) * 4
+    with _scope(name, stream, q, k, v, q_points, k_points, tau, q_group, k_group, lse, grad_out,
+                gq, gk, gv, gt, workspace):
+        gq = _out(name, gq, q.shape, b16, "grad_q", q.device)
+        gk = _out(name, gk, k.shape, b16, "grad_k", q.device)
+        gv = _out(name, gv, v.shape, b16, "grad_v", q.device)
+        gt = _out(name, gt, tau.shape, f32, "grad_tau", q.device) if tau is not None else None
+        need = int(lib().msda_query_attention_backward_workspace_size(p))
+        workspace = _workspace(need, q.device, workspace)
+        _check(lib().msda_query_attention_backward(
+            p, _ptr(lse), _ptr(grad_out), _ptr(gq), _ptr(gk), _ptr(gv), _ptr(gt),
+            _ptr(workspace), workspace.numel(), _stream(None)), name)
+    return gq, gk, gv, gt

@@ -163,3 +163,78 @@ def test_group_norm_backward_rejects(L, kw, code, fragment):
 def test_group_norm_of_no_items(L):
     assert _norm(L, d=(0, 16, 32, 2, 4), x=0, y=0, ws=0) == OK
     assert _norm_back(L, d=(0, 16, 32, 2, 4), x=0, gx=0, gy=0, mean=0, ws=0) == OK
+
+
+def _attention(**kw):
+    a = dict(q=FAKE, k=FAKE + (1 << 24), v=FAKE + (2 << 24), q_stride=64, k_stride=64, v_stride=128,
+             q_points=None, k_points=None, tau=None, q_group=None, k_group=None, scale=0.2, B=2,
+             Nq=10, Nk=300, H=2)
+    a.update(kw)
+    return msda.Attention(**a)
+
+
+def _attend(L, p, out=FAKE + (3 << 24), lse=FAKE + (4 << 24), ws=FAKE + (1 << 30), n=1 << 30):
+    return L.msda_query_attention(p, out, lse, ws, n, None)
+
+
+def _attend_back(L, p, lse=FAKE + (4 << 24), go=FAKE + (5 << 24), gq=FAKE + (6 << 24),
+                 gk=FAKE + (7 << 24), gv=FAKE + (8 << 24), gt=FAKE + (9 << 24),
+                 ws=FAKE + (1 << 30), n=1 << 30):
+    return L.msda_query_attention_backward(p, lse, go, gq, gk, gv, gt, ws, n, None)
+
+
+ATTENTION_BAD = [
+    (dict(B=-1), INVALID, "B (-1)"),
+    (dict(Nq=-1), INVALID, "Nq (-1)"),
+    (dict(Nk=-2), INVALID, "Nk (-2)"),
+    (dict(H=0), INVALID, "H (0)"),
+    (dict(H=2 ** 21, q_stride=2 ** 27), UNSUPPORTED, "H ="),
+    (dict(B=2 ** 30, Nq=2 ** 20), UNSUPPORTED, "too many rows"),
+    (dict(Nk=2 ** 31 - 1), UNSUPPORTED, "too many rows"),
+    (dict(scale=math.inf), INVALID, "scale"),
+    (dict(q=None), INVALID, "q is null"),
+    (dict(k=None), INVALID, "k is null"),
+    (dict(v=FAKE + 8), INVALID, "v must be 16-byte"),
+    (dict(q_stride=56), INVALID, "q_stride"),
+    (dict(k_stride=68), INVALID, "k_stride"),
+    (dict(v_stride=-64), INVALID, "v_stride"),
+    (dict(tau=FAKE), INVALID, "go together"),
+    (dict(q_points=FAKE, k_points=FAKE), INVALID, "go together"),
+    (dict(q_points=FAKE + 4, k_points=FAKE, tau=FAKE), INVALID, "8-byte"),
+    (dict(q_points=FAKE, k_points=FAKE, tau=FAKE + 2), INVALID, "4-byte"),
+    (dict(q_group=FAKE), INVALID, "go together"),
+    (dict(q_group=FAKE, k_group=FAKE + 1), INVALID, "4-byte"),
+]
+
+
+@pytest.mark.parametrize("kw,code,fragment", ATTENTION_BAD)
+def test_attention_rejects_bad_inputs(L, kw, code, fragment):
+    for call in (_attend, _attend_back):
+        assert call(L, _attention(**kw)) == code
+        assert fragment in L.msda_last_error().decode()
+    assert L.msda_query_attention(None, FAKE, FAKE, FAKE, 1 << 20, None) == INVALID
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(out=None), INVALID), (dict(out=FAKE + 8), INVALID), (dict(lse=FAKE + 2), INVALID),
+    (dict(out=FAKE), INVALID), (dict(out=FAKE + (2 << 24) + 64), INVALID),
+    (dict(ws=None), WORKSPACE), (dict(ws=FAKE + 16), WORKSPACE), (dict(n=100), WORKSPACE)])
+def test_attention_rejects_bad_outputs(L, kw, code):
+    assert L.msda_query_attention_workspace_size(_attention()) > 0   # keys are split here
+    assert _attend(L, _attention(), **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(lse=None), INVALID), (dict(go=None), INVALID), (dict(gq=None), INVALID),
+    (dict(gk=None), INVALID), (dict(gv=FAKE + 8), INVALID), (dict(gt=None), INVALID),
+    (dict(gk=FAKE), INVALID), (dict(ws=None), WORKSPACE), (dict(n=8), WORKSPACE)])
+def test_attention_backward_rejects_bad_outputs(L, kw, code):
+    p = _attention(q_points=FAKE, k_points=FAKE, tau=FAKE)
+    assert _attend_back(L, p, **kw) == code
+
+
+def test_attention_of_nothing(L):
+    for kw in (dict(B=0), dict(Nq=0)):
+        assert _attend(L, _attention(**kw, q=None), out=None, lse=None, ws=None, n=0) == OK
+    assert _attend_back(L, _attention(B=0, q=None, k=None, v=None), lse=None, go=None, gq=None,
+                        gk=None, gv=None, ws=None, n=0) == OK
