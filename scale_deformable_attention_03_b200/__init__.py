@@ -21,6 +21,7 @@ and ``msda_backward`` (``deterministic=True``: the fixed-point variants),
 entry points (workspace sizes, status strings, the no-alloc compaction, the
 GEMM's timeout counter and test switch) are reached through ``lib()``.
 """
+import contextlib
 import ctypes
 import operator
 import os
@@ -159,12 +160,12 @@ def lib():
         L.sca_forward_query_major.restype = ctypes.c_int
         L.msda_group_norm_workspace_size.argtypes = [NormDims]
         L.msda_group_norm_workspace_size.restype = ctypes.c_size_t
-        L.msda_group_norm.argtypes = [_vp, st, _i64p, _i64p, NormDims, _vp, _vp, ctypes.c_float,
+        L.msda_group_norm.argtypes = [_vp, st, _vp, _vp, NormDims, _vp, _vp, ctypes.c_float,
                                       st, st, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
         L.msda_group_norm.restype = ctypes.c_int
         L.msda_group_norm_backward_workspace_size.argtypes = [NormDims]
         L.msda_group_norm_backward_workspace_size.restype = ctypes.c_size_t
-        L.msda_group_norm_backward.argtypes = [_vp, st, _i64p, _i64p, NormDims, _vp, _vp, _vp,
+        L.msda_group_norm_backward.argtypes = [_vp, st, _vp, _vp, NormDims, _vp, _vp, _vp,
                                                _vp, st, _vp, st, st, _vp, _vp, _vp, _vp,
                                                ctypes.c_size_t, _vp]
         L.msda_group_norm_backward.restype = ctypes.c_int
@@ -244,19 +245,35 @@ def _contig(*ts):
             raise MsdaError("tensors must be contiguous")
 
 
-def _scope(name, stream, *ts):
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _scope(name, stream, first, *others):
     """The context of a call on the tensors' device: that device current and
     `stream` (of that device), when given, the current stream, so that what is
     allocated inside belongs to the stream that the kernels run on."""
     torch = _torch()
-    dev = ts[0].device
-    if any(t is not None and (not t.is_cuda or t.device != dev) for t in ts):
+    index = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != index:
+            index = -1
+    if index < 0:
         raise MsdaError(f"{name}: the tensors must be on one CUDA device")
-    if stream is None:
-        return torch.cuda.device(dev)
-    if stream.device != dev:
-        raise MsdaError(f"{name}: the stream is on {stream.device}, the tensors on {dev}")
-    return torch.cuda.stream(stream)
+    if stream is not None:
+        if stream.device.index != index:
+            raise MsdaError(f"{name}: the stream is on {stream.device}, the tensors on "
+                            f"{first.device}")
+        return torch.cuda.stream(stream)
+    return _HERE_ALREADY if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+
+def _raw_stream(tensor):
+    """The handle of the tensor's device's current stream (as an integer)."""
+    return _torch()._C._cuda_getCurrentRawStream(tensor.get_device())
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 def msda_forward(value, spatial_shapes, level_start_index, sampling_locations,
@@ -807,10 +824,10 @@ def msda_clip_grad_norm(grads, max_norm, eps=1e-6, grad_scale=1.0, out=None, tot
             raise MsdaError("msda_clip_grad_norm: total_norm must be one float32 value")
         workspace = _workspace(int(lib().msda_clip_grad_norm_workspace_size(n)), first.device,
                                workspace)
-        _check(lib().msda_clip_grad_norm(ctypes.c_void_p(table.ctypes.data), n, max_norm, eps,
-                                         grad_scale, _ptr(workspace),
+        _check(lib().msda_clip_grad_norm(table.ctypes.data, n, max_norm, eps,
+                                         grad_scale, _address(workspace),
                                          workspace.numel() * workspace.element_size(),
-                                         _ptr(total_norm), _stream(None)),
+                                         _address(total_norm), _raw_stream(first)),
                "msda_clip_grad_norm")
     return total_norm
 
@@ -822,7 +839,7 @@ def _arg(name, t, shape, dtypes, what):
     """An argument's shape, dtype and layout; None passes."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise MsdaError(f"{name}: {what} has the shape {list(t.shape)}, not {list(shape)}")
     if t.dtype not in dtypes:
         raise MsdaError(f"{name}: {what} is {t.dtype}")
@@ -879,11 +896,11 @@ def msda_group_norm(x, spatial_shapes, level_start_index, num_groups, gamma=None
         mean = _out(name, mean, small, f32, "mean", x.device)
         rstd = _out(name, rstd, small, f32, "rstd", x.device)
         workspace = _workspace(int(lib().msda_group_norm_workspace_size(d)), x.device, workspace)
-        _check(lib().msda_group_norm(_ptr(x), _vdt(x), shapes.ctypes.data_as(_i64p),
-                                     starts.ctypes.data_as(_i64p), d, _ptr(gamma), _ptr(beta),
-                                     eps, _ACTIVATIONS[activation], _vdt(y), _ptr(y), _ptr(mean),
-                                     _ptr(rstd), _ptr(workspace), workspace.numel(),
-                                     _stream(None)), name)
+        _check(lib().msda_group_norm(_address(x), _vdt(x), shapes.ctypes.data,
+                                     starts.ctypes.data, d, _address(gamma), _address(beta),
+                                     eps, _ACTIVATIONS[activation], _vdt(y), _address(y), _address(mean),
+                                     _address(rstd), _address(workspace), workspace.numel(),
+                                     _raw_stream(x)), name)
     return y, mean, rstd
 
 
@@ -913,10 +930,10 @@ def msda_group_norm_backward(x, spatial_shapes, level_start_index, num_groups, m
         workspace = _workspace(int(lib().msda_group_norm_backward_workspace_size(d)), x.device,
                                workspace)
         _check(lib().msda_group_norm_backward(
-            _ptr(x), _vdt(x), shapes.ctypes.data_as(_i64p), starts.ctypes.data_as(_i64p), d,
-            _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd), _ACTIVATIONS[activation],
-            _ptr(grad_out), _vdt(grad_out), _vdt(gx), _ptr(gx), _ptr(gg), _ptr(gb),
-            _ptr(workspace), workspace.numel(), _stream(None)), name)
+            _address(x), _vdt(x), shapes.ctypes.data, starts.ctypes.data, d,
+            _address(gamma), _address(beta), _address(mean), _address(rstd), _ACTIVATIONS[activation],
+            _address(grad_out), _vdt(grad_out), _vdt(gx), _address(gx), _address(gg), _address(gb),
+            _address(workspace), workspace.numel(), _raw_stream(x)), name)
     return gx, gg, gb
 
 
@@ -952,8 +969,8 @@ def _attention_args(name, q, k, v, q_points, k_points, tau, q_group, k_group, sc
         raise MsdaError(f"{name}: q_points, k_points and tau go together")
     if (q_group is None) != (k_group is None):
         raise MsdaError(f"{name}: q_group and k_group go together")
-    return Attention(_ptr(q), _ptr(k), _ptr(v), *strides, _ptr(q_points), _ptr(k_points),
-                     _ptr(tau), _ptr(q_group), _ptr(k_group),
+    return Attention(_address(q), _address(k), _address(v), *strides, _address(q_points), _address(k_points),
+                     _address(tau), _address(q_group), _address(k_group),
                      HEAD_DIM ** -0.5 if scale is None else scale, B, Nq, Nk, H)
 
 
@@ -976,9 +993,9 @@ def msda_query_attention(q, k, v, q_points=None, k_points=None, tau=None, q_grou
         need = int(lib().msda_query_attention_workspace_size(p))
         if need:
             workspace = _workspace(need, q.device, workspace)
-        _check(lib().msda_query_attention(p, _ptr(out), _ptr(lse), _ptr(workspace),
+        _check(lib().msda_query_attention(p, _address(out), _address(lse), _address(workspace),
                                           workspace.numel() if workspace is not None else 0,
-                                          _stream(None)), name)
+                                          _raw_stream(q)), name)
     return out, lse
 
 
@@ -1005,6 +1022,6 @@ def msda_query_attention_backward(q, k, v, lse, grad_out, q_points=None, k_point
         need = int(lib().msda_query_attention_backward_workspace_size(p))
         workspace = _workspace(need, q.device, workspace)
         _check(lib().msda_query_attention_backward(
-            p, _ptr(lse), _ptr(grad_out), _ptr(gq), _ptr(gk), _ptr(gv), _ptr(gt),
-            _ptr(workspace), workspace.numel(), _stream(None)), name)
+            p, _address(lse), _address(grad_out), _address(gq), _address(gk), _address(gv), _address(gt),
+            _address(workspace), workspace.numel(), _raw_stream(q)), name)
     return gq, gk, gv, gt

@@ -7,22 +7,28 @@
 // Backward, with xh = (x - mu) r, dz = dy act'(z), t = gamma dz:
 //   dgamma = sum dz xh, dbeta = sum dz, dx = r (t - mean(t) - xh mean(t xh))
 //
-// Both are two passes over the rows with a small merge between them: every
-// value needs sums over its whole level.  A pass takes chunks of rows, one CTA
-// each.  A thread holds eight neighbouring channels (16 bytes of bf16, 32 of
-// fp32) of kRowsPerThread rows, so its channels' constants stay in registers
-// and a warp reads whole rows.  The second pass walks the chunks backwards:
-// what the first one read last is still in L2.  The launches are programmatic
-// dependents of one another, so the second pass has its first rows in
-// registers while the merge ends.
+// Both are two passes over the rows, one launch each: every value needs sums
+// over its whole level.  The levels' rows of all items stand in one line, of
+// which each CTA takes an even run, whatever the levels' sizes; a run is cut
+// into spans at the levels' ends.  A thread holds two quads of channels of every
+// slots-th row of a span, so that a channel's constants and sums stay in
+// registers and only a span's end costs a reduction.  The quads are neighbours
+// where all tensors are bf16, else half a row apart: either way neighbouring
+// lanes' 16 bytes are neighbours (with the eight channels in one piece the two
+// loads of fp32 each took half of every sector: 66 us instead of 33 us for the
+// six cameras' first pass).  The first pass leaves one partial
+// result per span and group; the second adds those of its span's level (each
+// CTA for itself, in the same order: no atomic, no flag and no third launch)
+// and then walks its run backwards: what the first pass read last is still in
+// L2 (126 MB).  It is a programmatic dependent of the first.
 //
-// Bound by memory.  The three sums over a chunk stay in registers, then in
-// shared memory; a chunk leaves 16 bytes per group (forward) or 8 per channel
-// (backward), about 1 % of the data.
+// Bound by memory: the rows are read twice, the second time from L2 as far as
+// that reaches, and written once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "msda.h"
@@ -32,75 +38,119 @@ namespace msda {
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kRowsPerThread = 8;
+constexpr int kNormWarps = kNormThreads / 32;
 constexpr int kMaxC = MSDA_NORM_MAX_CHANNELS;
-constexpr int kMergeThreads = 512;  // 32 groups or channels wide, 16 chunks at a time
+constexpr int kSms = 148;
+constexpr int kMaxRuns = 2 * kSms;  // two CTAs per SM
 
 struct NormShape {
-    int B, Nv, C, L, G, cg;         // cg = C / G
-    int tpr, slots, chunk_rows;     // threads per row, rows at a time, rows per chunk
-    int chunks;                     // per item, over all levels
-    int start[kMaxLevels], rows[kMaxLevels], chunk0[kMaxLevels + 1];
-    int gaps, gap_chunks;           // runs of rows in no level
+    int B, Nv, C, L, G, cg;  // cg = C / G
+    int tpr, slots;          // threads per row, rows side by side
+    int runs;                // CTAs that share the rows
+    int used;                // rows of an item in its levels, cum[L]
+    int start[kMaxLevels], cum[kMaxLevels + 1];
+    int gaps;                // runs of rows in no level
     int gap_start[kMaxLevels + 1], gap_rows[kMaxLevels + 1];
 };
 
-struct ChunkAt {
-    int l, row, rows;  // level, first row within the item, rows
+// Run i holds the rows [total i / runs, total (i + 1) / runs) of the line of
+// all levels' rows.
+__device__ __forceinline__ int64_t run_begin(const NormShape& n, int i)
+{
+    return (int64_t)n.B * n.used * i / n.runs;
+}
+
+__device__ __forceinline__ int run_of(const NormShape& n, int64_t row)
+{
+    return (int)(((row + 1) * n.runs - 1) / ((int64_t)n.B * n.used));
+}
+
+// A span: rows [at, at + rows) of the line, all of one (item, level).
+struct Span {
+    int b, l, rows;
+    int64_t row;  // its first row among the tensor's B * Nv
 };
 
-__device__ __forceinline__ ChunkAt chunk_at(const NormShape& n, int chunk)
+__device__ __forceinline__ int level_of(const NormShape& n, int off)
 {
     int l = 0;
-    while (l + 1 < n.L && n.chunk0[l + 1] <= chunk) ++l;
-    const int at = (chunk - n.chunk0[l]) * n.chunk_rows;
-    return {l, n.start[l] + at, min(n.chunk_rows, n.rows[l] - at)};
+    while (l + 1 < n.L && n.cum[l + 1] <= off) ++l;
+    return l;
 }
+
+// The span that starts at `at` of a run that ends at `end`.
+__device__ __forceinline__ Span span_from(const NormShape& n, int64_t at, int64_t end)
+{
+    const int b = (int)(at / n.used), off = (int)(at - (int64_t)b * n.used);
+    const int l = level_of(n, off);
+    return {b, l, (int)min((int64_t)(n.cum[l + 1] - off), end - at),
+            (int64_t)b * n.Nv + n.start[l] + (off - n.cum[l])};
+}
+
+// The span that ends before `end` of a run that starts at `begin`.
+__device__ __forceinline__ Span span_before(const NormShape& n, int64_t begin, int64_t end)
+{
+    const int b = (int)((end - 1) / n.used);
+    const int l = level_of(n, (int)(end - 1 - (int64_t)b * n.used));
+    const int64_t first = max(begin, (int64_t)b * n.used + n.cum[l]);
+    return span_from(n, first, end);
+}
+
+// Where the partial results of run i's span of (item, level) bl lie: along the
+// line i or bl grows from each span to the next, so i + bl is their own.
+__device__ __forceinline__ int64_t span_slot(int run, int64_t bl) { return run + bl; }
 
 struct Vec8 {
     float v[8];
 };
 
-template <bool kBf16>
-struct Raw8 {  // eight values as they are stored
-    uint4 a[kBf16 ? 1 : 2];
+// A thread's channels: [a, a + 4) and [b, b + 4).
+struct Quads {
+    int a, b;
 };
 
-template <bool kBf16>
-__device__ __forceinline__ Raw8<kBf16> load8(const void* p, int64_t i)
+template <bool kSplit>
+__device__ __forceinline__ Quads quads_of(int C, int i)
 {
-    Raw8<kBf16> r;
-    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) +
-                                                    i * (kBf16 ? 2 : 4));
-    r.a[0] = __ldg(q);
-    if constexpr (!kBf16) r.a[1] = __ldg(q + 1);
-    return r;
+    if constexpr (kSplit) return {4 * i, C / 2 + 4 * i};
+    return {8 * i, 8 * i + 4};
+}
+
+__device__ __forceinline__ int channel(const Quads& q, int j) { return j < 4 ? q.a + j : q.b + j - 4; }
+
+__device__ __forceinline__ void widen_pair(float* o, uint32_t w)
+{
+    o[0] = __uint_as_float(w << 16);
+    o[1] = __uint_as_float(w & 0xffff0000u);
+}
+
+__device__ __forceinline__ Vec8 vec8(const float4& a, const float4& b)
+{
+    return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
 }
 
 template <bool kBf16>
-__device__ __forceinline__ Vec8 widen(const Raw8<kBf16>& r)
+__device__ __forceinline__ Vec8 load8(const void* p, int64_t row, const Quads& q)
 {
-    Vec8 o;
-    const uint32_t w[4] = {r.a[0].x, r.a[0].y, r.a[0].z, r.a[0].w};
     if constexpr (kBf16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            o.v[2 * i] = __uint_as_float(w[i] << 16);
-            o.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(p) + row;
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(h + q.a));
+        const uint2 b = __ldg(reinterpret_cast<const uint2*>(h + q.b));
+        Vec8 o;
+        widen_pair(o.v, a.x);
+        widen_pair(o.v + 2, a.y);
+        widen_pair(o.v + 4, b.x);
+        widen_pair(o.v + 6, b.y);
+        return o;
     } else {
-        const uint32_t u[4] = {r.a[1].x, r.a[1].y, r.a[1].z, r.a[1].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            o.v[i] = __uint_as_float(w[i]);
-            o.v[4 + i] = __uint_as_float(u[i]);
-        }
+        const float* f = static_cast<const float*>(p) + row;
+        return vec8(__ldg(reinterpret_cast<const float4*>(f + q.a)),
+                    __ldg(reinterpret_cast<const float4*>(f + q.b)));
     }
-    return o;
 }
 
-template <bool kBf16>
-__device__ __forceinline__ void store8(void* p, int64_t i, const Vec8& o)
+template <bool kBf16, bool kSplit>
+__device__ __forceinline__ void store8(void* p, int64_t row, const Quads& q, const Vec8& o)
 {
     if constexpr (kBf16) {
         uint32_t w[4];
@@ -109,26 +159,182 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const Vec8& o)
             const __nv_bfloat162 h = __floats2bfloat162_rn(o.v[2 * j], o.v[2 * j + 1]);
             w[j] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        __stcs(reinterpret_cast<uint4*>(static_cast<char*>(p) + i * 2),
-               make_uint4(w[0], w[1], w[2], w[3]));
+        __nv_bfloat16* h = static_cast<__nv_bfloat16*>(p) + row;
+        if constexpr (kSplit) {
+            __stcs(reinterpret_cast<uint2*>(h + q.a), make_uint2(w[0], w[1]));
+            __stcs(reinterpret_cast<uint2*>(h + q.b), make_uint2(w[2], w[3]));
+        } else {
+            __stcs(reinterpret_cast<uint4*>(h + q.a), make_uint4(w[0], w[1], w[2], w[3]));
+        }
     } else {
-        float4* q = reinterpret_cast<float4*>(static_cast<char*>(p) + i * 4);
-        __stcs(q, make_float4(o.v[0], o.v[1], o.v[2], o.v[3]));
-        __stcs(q + 1, make_float4(o.v[4], o.v[5], o.v[6], o.v[7]));
+        float* f = static_cast<float*>(p) + row;
+        __stcs(reinterpret_cast<float4*>(f + q.a), make_float4(o.v[0], o.v[1], o.v[2], o.v[3]));
+        __stcs(reinterpret_cast<float4*>(f + q.b), make_float4(o.v[4], o.v[5], o.v[6], o.v[7]));
     }
 }
 
-__device__ __forceinline__ Vec8 load_channels(const float* p, int64_t i, float otherwise)
+// A thread's rows on their way from memory: a ring in shared memory of kStages
+// steps of 64 bytes per thread (kStepRows rows of one tensor, or of x and dy),
+// written by asynchronous copies and read by the thread that asked for them
+// (no barrier).  With registers as the landing place a warp either waits for
+// its loads or computes: the memory then saw half of the requests it needs
+// (4.4 TB/s, against 160 KB in flight per SM here).
+constexpr int kStages = 5;
+constexpr int kRingBytes = kStages * 64 * kNormThreads;
+
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void* dst, const void* src)
 {
-    Vec8 o;
-    if (p == nullptr) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o.v[j] = otherwise;
-        return o;
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+__device__ __forceinline__ void copy_wait()  // for the oldest of kStages steps
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+}
+
+// A row's eight values in the ring: kPieces places of 16 bytes.
+template <bool kBf16, bool kSplit>
+struct RowCopy {
+    static constexpr int kPieces = kBf16 ? 1 : 2;
+    static __device__ __forceinline__ void fetch(uint4* to, const void* p, int64_t row,
+                                                 const Quads& q)
+    {
+        if constexpr (!kBf16) {
+            const float* f = static_cast<const float*>(p) + row;
+            copy_async<16>(to, f + q.a);
+            copy_async<16>(to + kNormThreads, f + q.b);
+        } else if constexpr (kSplit) {
+            const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(p) + row;
+            copy_async<8>(to, h + q.a);
+            copy_async<8>(reinterpret_cast<uint2*>(to) + 1, h + q.b);
+        } else {
+            copy_async<16>(to, static_cast<const __nv_bfloat16*>(p) + row + q.a);
+        }
     }
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p + i));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p + i) + 1);
-    o = {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+    static __device__ __forceinline__ Vec8 take(const uint4* from)
+    {
+        if constexpr (kBf16) {
+            const uint4 r = *from;
+            Vec8 o;
+            widen_pair(o.v, r.x);
+            widen_pair(o.v + 2, r.y);
+            widen_pair(o.v + 4, r.z);
+            widen_pair(o.v + 6, r.w);
+            return o;
+        } else {
+            return vec8(*reinterpret_cast<const float4*>(from),
+                        *reinterpret_cast<const float4*>(from + kNormThreads));
+        }
+    }
+};
+
+// Walks a thread's `count` rows, `step` values apart from the one that starts
+// at `first` on, through the ring: start() asks for the first steps, run()
+// calls use(row, x) or use(row, x, dy) for every row.
+template <bool kX, bool kSplit>
+struct Walk1 {
+    using Copy = RowCopy<kX, kSplit>;
+    static constexpr int kRows = 4 / Copy::kPieces;
+    uint4* ring;
+    const void* x;
+    Quads q;
+    int64_t first, step;
+    int count;
+
+    __device__ __forceinline__ uint4* at(int k, int i) const
+    {
+        return ring + ((k % kStages) * 4 + i * Copy::kPieces) * kNormThreads + threadIdx.x;
+    }
+    __device__ __forceinline__ void ask(int k) const
+    {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+            if (k * kRows + i < count)
+                Copy::fetch(at(k, i), x, first + (int64_t)(k * kRows + i) * step, q);
+        copy_commit();
+    }
+    __device__ __forceinline__ void start() const
+    {
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) ask(k);
+    }
+    template <typename F>
+    __device__ __forceinline__ void run(F use) const
+    {
+        for (int k = 0; k * kRows < count; ++k) {
+            ask(k + kStages - 1);
+            copy_wait();
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+                if (k * kRows + i < count)
+                    use(first + (int64_t)(k * kRows + i) * step, Copy::take(at(k, i)));
+        }
+    }
+};
+
+template <bool kX, bool kDy, bool kSplit>
+struct Walk2 {
+    using CopyX = RowCopy<kX, kSplit>;
+    using CopyD = RowCopy<kDy, kSplit>;
+    static constexpr int kPieces = CopyX::kPieces + CopyD::kPieces, kRows = 4 / kPieces;
+    uint4* ring;
+    const void *x, *dy;
+    Quads q;
+    int64_t first, step;
+    int count;
+
+    __device__ __forceinline__ uint4* at(int k, int i) const
+    {
+        return ring + ((k % kStages) * 4 + i * kPieces) * kNormThreads + threadIdx.x;
+    }
+    __device__ __forceinline__ void ask(int k) const
+    {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (k * kRows + i < count) {
+                const int64_t row = first + (int64_t)(k * kRows + i) * step;
+                CopyX::fetch(at(k, i), x, row, q);
+                CopyD::fetch(at(k, i) + CopyX::kPieces * kNormThreads, dy, row, q);
+            }
+        }
+        copy_commit();
+    }
+    __device__ __forceinline__ void start() const
+    {
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) ask(k);
+    }
+    template <typename F>
+    __device__ __forceinline__ void run(F use) const
+    {
+        for (int k = 0; k * kRows < count; ++k) {
+            ask(k + kStages - 1);
+            copy_wait();
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+                if (k * kRows + i < count)
+                    use(first + (int64_t)(k * kRows + i) * step, CopyX::take(at(k, i)),
+                        CopyD::take(at(k, i) + CopyX::kPieces * kNormThreads));
+        }
+    }
+};
+
+extern __shared__ uint4 ring_memory[];
+
+__device__ __forceinline__ Vec8 load_channels(const float* p, int64_t row, const Quads& q,
+                                              float otherwise)
+{
+    if (p != nullptr) return load8<false>(p, row, q);
+    Vec8 o;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o.v[j] = otherwise;
     return o;
 }
 
@@ -150,139 +356,155 @@ __device__ __forceinline__ void add_slots(float* s, int C, int slots)
     }
 }
 
-__device__ __forceinline__ void put_slot(float* s, int C, int slot, int c, const Vec8& a,
+__device__ __forceinline__ void put_slot(float* s, int C, int slot, const Quads& c, const Vec8& a,
                                          const Vec8& b)
 {
-    float* p = s + slot * C + c;
+    float* p = s + slot * C;
     float* q = p + kNormThreads * 8;
-#pragma unroll
-    for (int j = 0; j < 8; j += 4) {
-        *reinterpret_cast<float4*>(p + j) = make_float4(a.v[j], a.v[j + 1], a.v[j + 2], a.v[j + 3]);
-        *reinterpret_cast<float4*>(q + j) = make_float4(b.v[j], b.v[j + 1], b.v[j + 2], b.v[j + 3]);
-    }
+    *reinterpret_cast<float4*>(p + c.a) = make_float4(a.v[0], a.v[1], a.v[2], a.v[3]);
+    *reinterpret_cast<float4*>(p + c.b) = make_float4(a.v[4], a.v[5], a.v[6], a.v[7]);
+    *reinterpret_cast<float4*>(q + c.a) = make_float4(b.v[0], b.v[1], b.v[2], b.v[3]);
+    *reinterpret_cast<float4*>(q + c.b) = make_float4(b.v[4], b.v[5], b.v[6], b.v[7]);
+}
+
+// The 32 (or fewer) lanes that add up a group of cg channels: a power of two,
+// so that several small groups share a warp.
+struct GroupLanes {
+    int seg, per_warp, sub, in;
+};
+
+__device__ __forceinline__ GroupLanes group_lanes(int cg)
+{
+    int seg = 1;
+    while (seg < 32 && seg < cg) seg <<= 1;
+    const int lane = threadIdx.x & 31;
+    return {seg, 32 / seg, lane / seg, lane % seg};
+}
+
+__device__ __forceinline__ double add_lanes(double v, int seg)
+{
+    for (int o = seg >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
 // ---------------------------------------------------------------- forward
 
-// A chunk's mean and sum of squared distances from it, per group.  Within a
-// channel both come from sums relative to the chunk's first row (which keeps
-// their size that of the channel's spread), in fp32 over the chunk's rows; the
-// channels are merged in double.
+// A span's sums of x - m and of its square per group, m the mean of the group's
+// channels in the level's first row: the same for all spans of the level, so
+// that their sums add up, and near enough to the group's mean that nothing
+// cancels.  Within a channel the sums are fp32 and relative to the channel's
+// own value in that row; they are moved to m and added over the channels in
+// double.
 template <bool kX>
-__global__ void __launch_bounds__(kNormThreads) norm_stats_kernel(const void* __restrict__ x,
-                                                                  const NormShape n,
-                                                                  double2* __restrict__ part)
+__global__ void __launch_bounds__(kNormThreads, 2) norm_stats_kernel(const void* __restrict__ x,
+                                                                     const NormShape n,
+                                                                     double2* __restrict__ part,
+                                                                     double* __restrict__ middle)
 {
+    constexpr bool kSplit = !kX;
     __shared__ __align__(16) float s[2 * kNormThreads * 8];
     __shared__ float first[kMaxC];
     pdl_trigger();
-    const int b = blockIdx.x / n.chunks, chunk = blockIdx.x - b * n.chunks;
-    const ChunkAt at = chunk_at(n, chunk);
-    const int slot = threadIdx.x / n.tpr, c = (threadIdx.x - slot * n.tpr) * 8;
-    const int64_t base = ((int64_t)b * n.Nv + at.row) * n.C + c;
-    if (slot < n.slots) {
-        const Raw8<kX> r0 = load8<kX>(x, base);
-        Raw8<kX> r[kRowsPerThread];
-#pragma unroll
-        for (int i = 0; i < kRowsPerThread; ++i) {
-            const int row = slot + i * n.slots;
-            if (row < at.rows) r[i] = load8<kX>(x, base + (int64_t)row * n.C);
-        }
-        const Vec8 ref = widen(r0);
-        Vec8 a{}, q{};
-#pragma unroll
-        for (int i = 0; i < kRowsPerThread; ++i) {
-            if (slot + i * n.slots < at.rows) {
-                const Vec8 v = widen(r[i]);
+    const int slot = threadIdx.x / n.tpr;
+    const Quads c = quads_of<kSplit>(n.C, threadIdx.x - slot * n.tpr);
+    const GroupLanes gl = group_lanes(n.cg);
+    const int64_t end = run_begin(n, blockIdx.x + 1);
+    for (int64_t at = run_begin(n, blockIdx.x); at < end;) {
+        const Span sp = span_from(n, at, end);
+        if (slot < n.slots) {
+            const Walk1<kX, kSplit> walk{ring_memory,
+                                         x,
+                                         c,
+                                         (sp.row + slot) * n.C,
+                                         (int64_t)n.slots * n.C,
+                                         (sp.rows - slot + n.slots - 1) / n.slots};
+            walk.start();
+            const Vec8 ref = load8<kX>(x, ((int64_t)sp.b * n.Nv + n.start[sp.l]) * n.C, c);
+            Vec8 a{}, q{};
+            walk.run([&](int64_t, const Vec8& v) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float d = v.v[j] - ref.v[j];
                     a.v[j] += d;
                     q.v[j] = fmaf(d, d, q.v[j]);
                 }
+            });
+            put_slot(s, n.C, slot, c, a, q);
+            if (slot == 0) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) first[channel(c, j)] = ref.v[j];
             }
         }
-        put_slot(s, n.C, slot, c, a, q);
-        if (slot == 0) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) first[c + j] = ref.v[j];
+        add_slots(s, n.C, n.slots);
+        __syncthreads();
+        const double rows = (double)sp.rows;
+        const int64_t bl = (int64_t)sp.b * n.L + sp.l, to = span_slot(blockIdx.x, bl) * n.G;
+        const bool leads = at == (int64_t)sp.b * n.used + n.cum[sp.l];  // has the level's first row
+        for (int g0 = (threadIdx.x >> 5) * gl.per_warp; g0 < n.G; g0 += kNormWarps * gl.per_warp) {
+            const int g = g0 + gl.sub;
+            const bool on = g < n.G;
+            double m = 0.0, t1 = 0.0, t2 = 0.0;
+            for (int k = gl.in; on && k < n.cg; k += gl.seg) m += (double)first[g * n.cg + k];
+            m = add_lanes(m, gl.seg) / (double)n.cg;
+            for (int k = gl.in; on && k < n.cg; k += gl.seg) {
+                const int ch = g * n.cg + k;
+                const double a = s[ch], d = (double)first[ch] - m;
+                t1 += a + rows * d;
+                t2 += (double)s[kNormThreads * 8 + ch] + d * (2.0 * a + rows * d);
+            }
+            t1 = add_lanes(t1, gl.seg);
+            t2 = add_lanes(t2, gl.seg);
+            if (on && gl.in == 0) {
+                part[to + g] = make_double2(t1, t2);
+                if (leads) middle[bl * n.G + g] = m;
+            }
         }
-    }
-    add_slots(s, n.C, n.slots);
-    __syncthreads();
-    // lanes per group: a power of two, so that several small groups share a warp
-    int seg = 1;
-    while (seg < 32 && seg < n.cg) seg <<= 1;
-    const int per_warp = 32 / seg, lane = threadIdx.x & 31, sub = lane / seg, in = lane - sub * seg;
-    const double rows = (double)at.rows, inv_rows = 1.0 / rows;
-    for (int g0 = (threadIdx.x >> 5) * per_warp; g0 < n.G; g0 += (kNormThreads / 32) * per_warp) {
-        const int g = g0 + sub;
-        const bool on = g < n.G;
-        double sum = 0.0;
-        for (int k = in; on && k < n.cg; k += seg) {
-            const int ch = g * n.cg + k;
-            sum += (double)first[ch] + (double)s[ch] * inv_rows;
-        }
-        for (int o = seg >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const double mean = sum / (double)n.cg;
-        double m2 = 0.0;
-        for (int k = in; on && k < n.cg; k += seg) {
-            const int ch = g * n.cg + k;
-            const double a = s[ch], d = (double)first[ch] + a * inv_rows - mean;
-            m2 += (double)s[kNormThreads * 8 + ch] - a * a * inv_rows + rows * d * d;
-        }
-        for (int o = seg >> 1; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
-        if (on && in == 0) part[((int64_t)b * n.chunks + chunk) * n.G + g] = make_double2(mean, m2);
+        at += sp.rows;
+        __syncthreads();  // the sums are read before the next span's are written
     }
 }
 
-// Merges the chunks of one (item, level), 32 groups per CTA, in double and
-// relative to the first chunk's mean.  The mean is kept as two floats: what
-// the second pass subtracts is then exact to 48 bits, whatever the mean.
-__global__ void __launch_bounds__(kMergeThreads) norm_merge_kernel(
-    const double2* __restrict__ part, const NormShape n, float eps, float4* __restrict__ stats,
-    float* __restrict__ mean_out, float* __restrict__ rstd_out)
+// The partial results of all spans of an (item, level) for group g: one warp
+// per share of the spans, 32 groups at a time.
+struct Shares {
+    double2 s[kNormWarps][32];
+};
+
+__device__ __forceinline__ double2 add_spans(Shares& sh, const double2* part, const NormShape& n,
+                                             int b, int l, int g)
 {
-    __shared__ double2 s[kMergeThreads];
-    pdl_trigger();
-    const int b = blockIdx.x / n.L, l = blockIdx.x - b * n.L;
-    const int lane = threadIdx.x & 31, slot = threadIdx.x >> 5, g = blockIdx.y * 32 + lane;
-    const int k0 = n.chunk0[l], k1 = n.chunk0[l + 1];
-    const double2* p = part + ((int64_t)b * n.chunks) * n.G + g;
-    double a = 0.0, q = 0.0, ref = 0.0;
-    pdl_wait();
+    const int64_t lo = (int64_t)b * n.used + n.cum[l], hi = (int64_t)b * n.used + n.cum[l + 1];
+    const int r0 = run_of(n, lo), r1 = run_of(n, hi - 1);
+    const int64_t bl = (int64_t)b * n.L + l;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    double2 acc = make_double2(0.0, 0.0);
     if (g < n.G) {
-        ref = p[(int64_t)k0 * n.G].x;
-#pragma unroll 4
-        for (int k = k0 + slot; k < k1; k += kMergeThreads / 32) {
-            const double2 v = p[(int64_t)k * n.G];
-            const int rows = min(n.chunk_rows, n.rows[l] - (k - k0) * n.chunk_rows);
-            const double w = (double)rows * n.cg, d = v.x - ref;
-            a += w * d;
-            q += v.y + w * d * d;
+#pragma unroll 8
+        for (int r = r0 + warp; r <= r1; r += kNormWarps) {
+            const double2 v = part[span_slot(r, bl) * n.G + g];
+            acc.x += v.x;
+            acc.y += v.y;
         }
     }
-    s[threadIdx.x] = make_double2(a, q);
+    sh.s[warp][lane] = acc;
     __syncthreads();
-    if (slot == 0 && g < n.G) {
-        for (int k = 1; k < kMergeThreads / 32; ++k) {
-            a += s[k * 32 + lane].x;
-            q += s[k * 32 + lane].y;
+    if (warp == 0) {
+        for (int k = 1; k < kNormWarps; ++k) {
+            acc.x += sh.s[k][lane].x;
+            acc.y += sh.s[k][lane].y;
         }
-        const double N = (double)n.rows[l] * n.cg;
-        const double mean = ref + a / N;
-        double var = (q - a * a / N) / N;
-        if (var < 0.0) var = 0.0;  // rounding only; a NaN stays
-        const double r = 1.0 / sqrt(var + (double)eps);
-        const float hi = (float)mean;
-        const int64_t i = ((int64_t)b * n.L + l) * n.G + g;
-        stats[i] = make_float4(hi, (float)(mean - (double)hi), (float)r, 0.0f);
-        if (mean_out) mean_out[i] = hi;
-        if (rstd_out) rstd_out[i] = (float)r;
     }
+    return acc;  // for warp 0; a barrier before `sh` is used again
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
+// An approximate reciprocal (one unit in the last place) instead of a division,
+// which would bind the bf16 passes by instruction issue.
+__device__ __forceinline__ float sigmoid(float z)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-z)));
+    return r;
+}
 
 template <int kAct>
 __device__ __forceinline__ float activate(float z)
@@ -292,69 +514,93 @@ __device__ __forceinline__ float activate(float z)
     return z;
 }
 
-// Rows of no level: zeros.
+// Rows of no level: zeros, an even share per CTA.
 template <bool kY>
-__device__ void zero_gap(const NormShape& n, void* y, int b, int gap_chunk)
+__device__ void zero_gaps(const NormShape& n, void* y, int cta, int ctas)
 {
-    int k = 0;
-    for (; k < n.gaps; ++k) {
-        const int c = (n.gap_rows[k] + n.chunk_rows - 1) / n.chunk_rows;
-        if (gap_chunk < c) break;
-        gap_chunk -= c;
+    for (int k = 0; k < n.gaps; ++k) {
+        const int64_t per = (int64_t)n.gap_rows[k] * n.tpr, all = per * n.B;
+        for (int64_t i = (int64_t)cta * kNormThreads + threadIdx.x; i < all;
+             i += (int64_t)ctas * kNormThreads) {
+            const int64_t b = i / per;
+            const int64_t at = (b * n.Nv + n.gap_start[k]) * n.C + (i - b * per) * 8;
+            store8<kY, true>(y, at, {0, 4}, Vec8{});
+        }
     }
-    if (k == n.gaps) return;
-    const int row0 = gap_chunk * n.chunk_rows;
-    const int rows = min(n.chunk_rows, n.gap_rows[k] - row0);
-    const int64_t base = ((int64_t)b * n.Nv + n.gap_start[k] + row0) * n.C;
-    for (int i = threadIdx.x; i < rows * n.tpr; i += kNormThreads)
-        store8<kY>(y, base + (int64_t)i * 8, Vec8{});
 }
 
 template <bool kX, bool kY, int kAct>
-__global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(
-    const void* __restrict__ x, const NormShape n, const float4* __restrict__ stats,
-    const float* __restrict__ gamma, const float* __restrict__ beta, void* __restrict__ y)
+__global__ void __launch_bounds__(kNormThreads, 2) norm_apply_kernel(
+    const void* __restrict__ x, const NormShape n, const double2* __restrict__ part,
+    const double* __restrict__ middle, float eps,
+    const float* __restrict__ gamma, const float* __restrict__ beta, void* __restrict__ y,
+    float* __restrict__ mean_out, float* __restrict__ rstd_out)
 {
-    const int per = n.chunks + n.gap_chunks;
-    const int id = gridDim.x - 1 - blockIdx.x;
-    const int b = id / per, chunk = id - b * per;
-    if (chunk >= n.chunks) {
-        pdl_wait();
-        zero_gap<kY>(n, y, b, chunk - n.chunks);
-        return;
-    }
-    const ChunkAt at = chunk_at(n, chunk);
-    const int slot = threadIdx.x / n.tpr, c = (threadIdx.x - slot * n.tpr) * 8;
-    if (slot >= n.slots) return;
-    const int64_t base = ((int64_t)b * n.Nv + at.row) * n.C + c;
-    Raw8<kX> r[kRowsPerThread];
-#pragma unroll
-    for (int i = 0; i < kRowsPerThread; ++i) {
-        const int row = slot + i * n.slots;
-        if (row < at.rows) r[i] = load8<kX>(x, base + (int64_t)row * n.C);
-    }
-    const Vec8 ga = load_channels(gamma, (int64_t)at.l * n.C + c, 1.0f);
-    const Vec8 be = load_channels(beta, (int64_t)at.l * n.C + c, 0.0f);
-    Vec8 hi, lo, a;
-    pdl_wait();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float4 st = stats[((int64_t)b * n.L + at.l) * n.G + (c + j) / n.cg];
-        hi.v[j] = st.x;
-        lo.v[j] = st.y;
-        a.v[j] = st.z * ga.v[j];
-    }
-#pragma unroll
-    for (int i = 0; i < kRowsPerThread; ++i) {
-        const int row = slot + i * n.slots;
-        if (row < at.rows) {
-            Vec8 v = widen(r[i]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v.v[j] = activate<kAct>(fmaf((v.v[j] - hi.v[j]) - lo.v[j], a.v[j], be.v[j]));
-            store8<kY>(y, base + (int64_t)row * n.C, v);
+    constexpr bool kSplit = !(kX && kY);
+    __shared__ Shares shares;
+    // the mean as two floats: what is subtracted is exact to 48 bits, whatever the mean
+    __shared__ float st_hi[kMaxC], st_lo[kMaxC], st_r[kMaxC];
+    const int run = n.runs - 1 - (int)blockIdx.x;
+    const int slot = threadIdx.x / n.tpr;
+    const Quads c = quads_of<kSplit>(n.C, threadIdx.x - slot * n.tpr);
+    const int64_t begin = run_begin(n, run);
+    bool waited = false;
+    for (int64_t end = run_begin(n, run + 1); end > begin;) {
+        const Span sp = span_before(n, begin, end);
+        // the span's rows from its last on (what the pass before read last)
+        const Walk1<kX, kSplit> walk{
+            ring_memory,
+            x,
+            c,
+            (sp.row + sp.rows - 1 - slot) * n.C,
+            -(int64_t)n.slots * n.C,
+            slot < n.slots ? (sp.rows - slot + n.slots - 1) / n.slots : 0};
+        walk.start();
+        if (!waited) pdl_wait();  // nothing that the pass before writes is read above
+        waited = true;
+        const int64_t bl = (int64_t)sp.b * n.L + sp.l;
+        for (int g0 = 0; g0 < n.G; g0 += 32) {
+            const int g = g0 + (threadIdx.x & 31);
+            const double2 acc = add_spans(shares, part, n, sp.b, sp.l, g);
+            if (threadIdx.x < 32 && g < n.G) {
+                const double N = (double)(n.cum[sp.l + 1] - n.cum[sp.l]) * n.cg;
+                const double mean = middle[bl * n.G + g] + acc.x / N;
+                double var = (acc.y - acc.x * acc.x / N) / N;
+                if (var < 0.0) var = 0.0;  // rounding only; a NaN stays
+                const float hi = (float)mean, r = (float)(1.0 / sqrt(var + (double)eps));
+                st_hi[g] = hi;
+                st_lo[g] = (float)(mean - (double)hi);
+                st_r[g] = r;
+                // the run with the level's first row writes the statistics
+                if (begin <= (int64_t)sp.b * n.used + n.cum[sp.l]) {
+                    if (mean_out) mean_out[bl * n.G + g] = hi;
+                    if (rstd_out) rstd_out[bl * n.G + g] = r;
+                }
+            }
+            __syncthreads();
         }
+        if (slot < n.slots) {
+            const Vec8 ga = load_channels(gamma, (int64_t)sp.l * n.C, c, 1.0f);
+            const Vec8 be = load_channels(beta, (int64_t)sp.l * n.C, c, 0.0f);
+            Vec8 hi, lo, a;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int g = channel(c, j) / n.cg;
+                hi.v[j] = st_hi[g];
+                lo.v[j] = st_lo[g];
+                a.v[j] = st_r[g] * ga.v[j];
+            }
+            walk.run([&](int64_t at, Vec8 v) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v.v[j] = activate<kAct>(fmaf((v.v[j] - hi.v[j]) - lo.v[j], a.v[j], be.v[j]));
+                store8<kY, kSplit>(y, at, c, v);
+            });
+        }
+        end -= sp.rows;
+        __syncthreads();  // the statistics are read before the next span's are written
     }
+    zero_gaps<kY>(n, y, blockIdx.x, gridDim.x);
 }
 
 // --------------------------------------------------------------- backward
@@ -383,229 +629,195 @@ struct Channels {
     Vec8 mean, rstd, gamma, beta;
 };
 
-__device__ __forceinline__ Channels load_constants(const NormShape& n, int b, int l, int c,
+__device__ __forceinline__ Channels load_constants(const NormShape& n, int b, int l,
+                                                   const Quads& c,
                                                    const float* mean, const float* rstd,
                                                    const float* gamma, const float* beta)
 {
     Channels k;
-    k.gamma = load_channels(gamma, (int64_t)l * n.C + c, 1.0f);
-    k.beta = load_channels(beta, (int64_t)l * n.C + c, 0.0f);
+    k.gamma = load_channels(gamma, (int64_t)l * n.C, c, 1.0f);
+    k.beta = load_channels(beta, (int64_t)l * n.C, c, 0.0f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int64_t i = ((int64_t)b * n.L + l) * n.G + (c + j) / n.cg;
+        const int64_t i = ((int64_t)b * n.L + l) * n.G + channel(c, j) / n.cg;
         k.mean.v[j] = __ldg(mean + i);
         k.rstd.v[j] = __ldg(rstd + i);
     }
     return k;
 }
 
-constexpr int kBackRows = 4;  // rows in flight: two tensors are read
-
+// A span's sums of dz and dz xh per channel (fp32, for the parameters'
+// gradients) and, weighted with gamma, per group (double, for dx).
 template <bool kX, bool kDy, int kAct>
-__global__ void __launch_bounds__(kNormThreads) norm_grad_sums_kernel(
+__global__ void __launch_bounds__(kNormThreads, 2) norm_grad_sums_kernel(
     const void* __restrict__ x, const void* __restrict__ dy, const NormShape n,
     const float* __restrict__ mean, const float* __restrict__ rstd,
-    const float* __restrict__ gamma, const float* __restrict__ beta, float* __restrict__ part)
+    const float* __restrict__ gamma, const float* __restrict__ beta, float* __restrict__ chan,
+    double2* __restrict__ part)
 {
+    constexpr bool kSplit = !(kX && kDy);
     __shared__ __align__(16) float s[2 * kNormThreads * 8];
     pdl_trigger();
-    const int b = blockIdx.x / n.chunks, chunk = blockIdx.x - b * n.chunks;
-    const ChunkAt at = chunk_at(n, chunk);
-    const int slot = threadIdx.x / n.tpr, c = (threadIdx.x - slot * n.tpr) * 8;
-    if (slot < n.slots) {
-        const int64_t base = ((int64_t)b * n.Nv + at.row) * n.C + c;
-        const Channels k = load_constants(n, b, at.l, c, mean, rstd, gamma, beta);
-        Vec8 a{}, q{};
+    const int slot = threadIdx.x / n.tpr;
+    const Quads c = quads_of<kSplit>(n.C, threadIdx.x - slot * n.tpr);
+    const GroupLanes gl = group_lanes(n.cg);
+    const int64_t end = run_begin(n, blockIdx.x + 1);
+    for (int64_t at = run_begin(n, blockIdx.x); at < end;) {
+        const Span sp = span_from(n, at, end);
+        if (slot < n.slots) {
+            const Walk2<kX, kDy, kSplit> walk{ring_memory,
+                                              x,
+                                              dy,
+                                              c,
+                                              (sp.row + slot) * n.C,
+                                              (int64_t)n.slots * n.C,
+                                              (sp.rows - slot + n.slots - 1) / n.slots};
+            walk.start();
+            const Channels k = load_constants(n, sp.b, sp.l, c, mean, rstd, gamma, beta);
+            Vec8 a{}, q{};
+            walk.run([&](int64_t, const Vec8& v, const Vec8& d) {
 #pragma unroll
-        for (int i0 = 0; i0 < kRowsPerThread; i0 += kBackRows) {
-            Raw8<kX> rx[kBackRows];
-            Raw8<kDy> rd[kBackRows];
-#pragma unroll
-            for (int i = 0; i < kBackRows; ++i) {
-                const int row = slot + (i0 + i) * n.slots;
-                if (row < at.rows) {
-                    rx[i] = load8<kX>(x, base + (int64_t)row * n.C);
-                    rd[i] = load8<kDy>(dy, base + (int64_t)row * n.C);
+                for (int j = 0; j < 8; ++j) {
+                    const float hat = (v.v[j] - k.mean.v[j]) * k.rstd.v[j];
+                    const float dz = grad_z<kAct>(d.v[j], v.v[j], k.mean.v[j], k.rstd.v[j], hat,
+                                                  k.gamma.v[j], k.beta.v[j]);
+                    a.v[j] += dz;
+                    q.v[j] = fmaf(dz, hat, q.v[j]);
                 }
-            }
-#pragma unroll
-            for (int i = 0; i < kBackRows; ++i) {
-                if (slot + (i0 + i) * n.slots < at.rows) {
-                    const Vec8 v = widen(rx[i]), d = widen(rd[i]);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float hat = (v.v[j] - k.mean.v[j]) * k.rstd.v[j];
-                        const float dz = grad_z<kAct>(d.v[j], v.v[j], k.mean.v[j], k.rstd.v[j],
-                                                      hat, k.gamma.v[j], k.beta.v[j]);
-                        a.v[j] += dz;
-                        q.v[j] = fmaf(dz, hat, q.v[j]);
-                    }
-                }
-            }
+            });
+            put_slot(s, n.C, slot, c, a, q);
         }
-        put_slot(s, n.C, slot, c, a, q);
-    }
-    add_slots(s, n.C, n.slots);
-    float* out = part + ((int64_t)b * n.chunks + chunk) * 2 * n.C;
-    for (int ch = threadIdx.x; ch < n.C; ch += kNormThreads) {  // the channels it has added itself
-        out[ch] = s[ch];
-        out[n.C + ch] = s[kNormThreads * 8 + ch];
+        add_slots(s, n.C, n.slots);
+        __syncthreads();
+        const int64_t to = span_slot(blockIdx.x, (int64_t)sp.b * n.L + sp.l);
+        for (int ch = threadIdx.x; ch < n.C; ch += kNormThreads) {
+            chan[to * 2 * n.C + ch] = s[ch];
+            chan[to * 2 * n.C + n.C + ch] = s[kNormThreads * 8 + ch];
+        }
+        for (int g0 = (threadIdx.x >> 5) * gl.per_warp; g0 < n.G; g0 += kNormWarps * gl.per_warp) {
+            const int g = g0 + gl.sub;
+            const bool on = g < n.G;
+            double t1 = 0.0, t2 = 0.0;
+            for (int k = gl.in; on && k < n.cg; k += gl.seg) {
+                const int ch = g * n.cg + k;
+                const double w = gamma ? (double)__ldg(gamma + (int64_t)sp.l * n.C + ch) : 1.0;
+                t1 += w * (double)s[ch];
+                t2 += w * (double)s[kNormThreads * 8 + ch];
+            }
+            t1 = add_lanes(t1, gl.seg);
+            t2 = add_lanes(t2, gl.seg);
+            if (on && gl.in == 0) part[to * n.G + g] = make_double2(t1, t2);
+        }
+        at += sp.rows;
+        __syncthreads();
     }
 }
 
-// Adds the chunks of one (item, level) per channel, in double, then the
-// channels of each group: grid (B * L, blocks of whole groups), a block of
-// groups at least 32 channels wide where the groups are smaller.
-__global__ void __launch_bounds__(kMergeThreads) norm_grad_merge_kernel(
-    const float* __restrict__ part, const NormShape n, int groups_per_block,
-    const float* __restrict__ gamma, double2* __restrict__ chan, float2* __restrict__ coef)
+// Level l's parameter gradients, 32 channels of them: the channel sums of all
+// its spans in double, one warp per share of the spans.
+__device__ __forceinline__ void add_parameters(Shares& sh, const float* chan, const NormShape& n,
+                                               int l, int c, float* dgamma, float* dbeta)
 {
-    __shared__ double2 s[kMergeThreads];
-    pdl_trigger();
-    const int b = blockIdx.x / n.L, l = blockIdx.x - b * n.L;
-    const int lane = threadIdx.x & 31, slot = threadIdx.x >> 5;
-    const int g0 = blockIdx.y * groups_per_block;
-    const int c0 = g0 * n.cg, c1 = min(n.C, (g0 + groups_per_block) * n.cg);
-    const double inv = 1.0 / ((double)n.rows[l] * n.cg);
-    const float* p = part + (int64_t)b * n.chunks * 2 * n.C;
-    double t1 = 0.0, t2 = 0.0;  // a group wider than the block: its sums so far (lane 0)
-    pdl_wait();
-    for (int cb = c0; cb < c1; cb += 32) {
-        const int c = cb + lane;
-        double a = 0.0, q = 0.0;
-        if (c < c1) {
-#pragma unroll 4
-            for (int k = n.chunk0[l] + slot; k < n.chunk0[l + 1]; k += kMergeThreads / 32) {
-                a += (double)p[(int64_t)k * 2 * n.C + c];
-                q += (double)p[(int64_t)k * 2 * n.C + n.C + c];
-            }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    double2 acc = make_double2(0.0, 0.0);
+    for (int b = 0; b < n.B; ++b) {
+        const int64_t lo = (int64_t)b * n.used + n.cum[l], hi = (int64_t)b * n.used + n.cum[l + 1];
+        const int r0 = run_of(n, lo), r1 = run_of(n, hi - 1);
+#pragma unroll 8
+        for (int r = r0 + warp; c < n.C && r <= r1; r += kNormWarps) {
+            const float* p = chan + span_slot(r, (int64_t)b * n.L + l) * 2 * n.C + c;
+            acc.x += (double)p[0];
+            acc.y += (double)p[n.C];
         }
-        s[threadIdx.x] = make_double2(a, q);
-        __syncthreads();
-        if (slot == 0) {
-            for (int k = 1; k < kMergeThreads / 32; ++k) {
-                a += s[k * 32 + lane].x;
-                q += s[k * 32 + lane].y;
-            }
-            if (c < c1) chan[((int64_t)b * n.L + l) * n.C + c] = make_double2(a, q);
-            const double w = c < c1 && gamma != nullptr ? (double)gamma[(int64_t)l * n.C + c] : 1.0;
-            a *= w;
-            q *= w;
-            if (n.cg > 32) {
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    a += __shfl_xor_sync(0xffffffffu, a, o);
-                    q += __shfl_xor_sync(0xffffffffu, q, o);
-                }
-                t1 += a;
-                t2 += q;
-            } else {
-                __syncwarp();
-                s[lane] = make_double2(a, q);
-                __syncwarp();
-                const int g = g0 + lane;
-                if (lane < groups_per_block && g < n.G) {
-                    double u1 = 0.0, u2 = 0.0;
-                    for (int k = 0; k < n.cg; ++k) {
-                        u1 += s[lane * n.cg + k].x;
-                        u2 += s[lane * n.cg + k].y;
-                    }
-                    coef[((int64_t)b * n.L + l) * n.G + g] =
-                        make_float2((float)(u1 * inv), (float)(u2 * inv));
-                }
-            }
-        }
-        __syncthreads();
     }
-    if (n.cg > 32 && threadIdx.x == 0)
-        coef[((int64_t)b * n.L + l) * n.G + g0] = make_float2((float)(t1 * inv), (float)(t2 * inv));
+    sh.s[warp][lane] = acc;
+    __syncthreads();
+    if (warp == 0 && c < n.C) {
+        for (int k = 1; k < kNormWarps; ++k) {
+            acc.x += sh.s[k][lane].x;
+            acc.y += sh.s[k][lane].y;
+        }
+        if (dbeta) dbeta[(int64_t)l * n.C + c] = (float)acc.x;
+        if (dgamma) dgamma[(int64_t)l * n.C + c] = (float)acc.y;
+    }
 }
 
 template <bool kX, bool kDy, bool kDx, int kAct>
-__global__ void __launch_bounds__(kNormThreads) norm_grad_apply_kernel(
+__global__ void __launch_bounds__(kNormThreads, 2) norm_grad_apply_kernel(
     const void* __restrict__ x, const void* __restrict__ dy, const NormShape n,
     const float* __restrict__ mean, const float* __restrict__ rstd,
     const float* __restrict__ gamma, const float* __restrict__ beta,
-    const double2* __restrict__ chan, const float2* __restrict__ coef, void* __restrict__ dx,
+    const float* __restrict__ chan, const double2* __restrict__ part, void* __restrict__ dx,
     float* __restrict__ dgamma, float* __restrict__ dbeta)
 {
-    const int per = n.chunks + n.gap_chunks;
-    const int id = n.B * per - 1 - (int)blockIdx.x;
-    if (id < 0) {  // the CTAs behind the last chunk add the items' parameter gradients
-        const int i = (-1 - id) * kNormThreads + (int)threadIdx.x;
-        if (i >= n.L * n.C) return;
+    constexpr bool kSplit = !(kX && kDy && kDx);
+    __shared__ Shares shares;
+    __shared__ float c1s[kMaxC], c2s[kMaxC];
+    if ((int)blockIdx.x >= n.runs) {  // the CTAs behind the runs: parameter gradients
         pdl_wait();
-        double a = 0.0, q = 0.0;
-        for (int b = 0; b < n.B; ++b) {
-            const double2 v = chan[(int64_t)b * n.L * n.C + i];
-            a += v.x;
-            q += v.y;
-        }
-        if (dbeta) dbeta[i] = (float)a;
-        if (dgamma) dgamma[i] = (float)q;
+        const int i = blockIdx.x - n.runs, blocks = (n.C + 31) / 32, l = i / blocks;
+        add_parameters(shares, chan, n, l, (i - l * blocks) * 32 + (threadIdx.x & 31), dgamma,
+                       dbeta);
         return;
     }
-    const int b = id / per, chunk = id - b * per;
-    if (chunk >= n.chunks) {
-        pdl_wait();
-        zero_gap<kDx>(n, dx, b, chunk - n.chunks);
-        return;
-    }
-    const ChunkAt at = chunk_at(n, chunk);
-    const int slot = threadIdx.x / n.tpr, c = (threadIdx.x - slot * n.tpr) * 8;
-    if (slot >= n.slots) return;
-    const int64_t base = ((int64_t)b * n.Nv + at.row) * n.C + c;
-    const Channels k = load_constants(n, b, at.l, c, mean, rstd, gamma, beta);
-    Vec8 c1, c2;
-#pragma unroll
-    for (int i0 = 0; i0 < kRowsPerThread; i0 += kBackRows) {
-        Raw8<kX> rx[kBackRows];
-        Raw8<kDy> rd[kBackRows];
-#pragma unroll
-        for (int i = 0; i < kBackRows; ++i) {
-            const int row = slot + (i0 + i) * n.slots;
-            if (row < at.rows) {
-                rx[i] = load8<kX>(x, base + (int64_t)row * n.C);
-                rd[i] = load8<kDy>(dy, base + (int64_t)row * n.C);
+    const int run = n.runs - 1 - (int)blockIdx.x;
+    const int slot = threadIdx.x / n.tpr;
+    const Quads c = quads_of<kSplit>(n.C, threadIdx.x - slot * n.tpr);
+    const int64_t begin = run_begin(n, run);
+    bool waited = false;
+    for (int64_t end = run_begin(n, run + 1); end > begin;) {
+        const Span sp = span_before(n, begin, end);
+        const Walk2<kX, kDy, kSplit> walk{
+            ring_memory,
+            x,
+            dy,
+            c,
+            (sp.row + sp.rows - 1 - slot) * n.C,
+            -(int64_t)n.slots * n.C,
+            slot < n.slots ? (sp.rows - slot + n.slots - 1) / n.slots : 0};
+        walk.start();
+        if (!waited) pdl_wait();
+        waited = true;
+        const double inv = 1.0 / ((double)(n.cum[sp.l + 1] - n.cum[sp.l]) * n.cg);
+        for (int g0 = 0; g0 < n.G; g0 += 32) {
+            const int g = g0 + (threadIdx.x & 31);
+            const double2 acc = add_spans(shares, part, n, sp.b, sp.l, g);
+            if (threadIdx.x < 32 && g < n.G) {
+                c1s[g] = (float)(acc.x * inv);
+                c2s[g] = (float)(acc.y * inv);
             }
+            __syncthreads();
         }
-        if (i0 == 0) {
-            pdl_wait();
+        if (slot < n.slots) {
+            const Channels k = load_constants(n, sp.b, sp.l, c, mean, rstd, gamma, beta);
+            Vec8 c1, c2;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float2 v = coef[((int64_t)b * n.L + at.l) * n.G + (c + j) / n.cg];
-                c1.v[j] = v.x;
-                c2.v[j] = v.y;
+                c1.v[j] = c1s[channel(c, j) / n.cg];
+                c2.v[j] = c2s[channel(c, j) / n.cg];
             }
-        }
-#pragma unroll
-        for (int i = 0; i < kBackRows; ++i) {
-            const int row = slot + (i0 + i) * n.slots;
-            if (row < at.rows) {
-                const Vec8 v = widen(rx[i]), d = widen(rd[i]);
+            walk.run([&](int64_t at, const Vec8& v, const Vec8& d) {
                 Vec8 o;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float hat = (v.v[j] - k.mean.v[j]) * k.rstd.v[j];
                     const float dz = grad_z<kAct>(d.v[j], v.v[j], k.mean.v[j], k.rstd.v[j], hat,
                                                   k.gamma.v[j], k.beta.v[j]);
-                    // t rounded before the mean is taken off: exactly 0 where
-                    // the group has one value
+                    // t rounded before the mean is taken off: exactly 0 where the
+                    // group has one value
                     const float t = __fmul_rn(k.gamma.v[j], dz);
                     o.v[j] = k.rstd.v[j] * fmaf(-hat, c2.v[j], __fsub_rn(t, c1.v[j]));
                 }
-                store8<kDx>(dx, base + (int64_t)row * n.C, o);
-            }
+                store8<kDx, kSplit>(dx, at, c, o);
+            });
         }
+        end -= sp.rows;
+        __syncthreads();
     }
+    zero_gaps<kDx>(n, dx, blockIdx.x, n.runs);
 }
 
 // ------------------------------------------------------------------- host
-
-int norm_chunk_rows(int C)
-{
-    return std::max(1, kNormThreads / (C / 8)) * kRowsPerThread;
-}
 
 bool norm_sizes_ok(const msda_norm_dims_t& d)
 {
@@ -613,10 +825,10 @@ bool norm_sizes_ok(const msda_norm_dims_t& d)
            d.L <= MSDA_MAX_LEVELS && d.G >= 1 && d.C % d.G == 0;
 }
 
-// Chunks per item, at most: whole ones over all rows and one cut per level.
-int64_t norm_max_chunks(const msda_norm_dims_t& d)
+// Spans, at most: each starts where a run or a level does.
+size_t norm_max_spans(const msda_norm_dims_t& d)
 {
-    return d.Nv / norm_chunk_rows(d.C) + d.L;
+    return (size_t)kMaxRuns + (size_t)d.B * d.L;
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -645,7 +857,6 @@ msda_status_t norm_shape(const msda_norm_dims_t& d, const int64_t* shapes, const
     n.cg = d.C / d.G;
     n.tpr = d.C / 8;
     n.slots = std::max(1, kNormThreads / n.tpr);
-    n.chunk_rows = norm_chunk_rows(d.C);
     int order[MSDA_MAX_LEVELS];
     for (int l = 0; l < d.L; ++l) {
         const int64_t h = shapes[2 * l], w = shapes[2 * l + 1], st = starts[l];
@@ -657,14 +868,15 @@ msda_status_t norm_shape(const msda_norm_dims_t& d, const int64_t* shapes, const
                              "level %d (start %lld, %lld x %lld) does not fit in Nv = %d", l,
                              (long long)st, (long long)h, (long long)w, d.Nv);
         n.start[l] = (int)st;
-        n.rows[l] = (int)(h * w);
-        n.chunk0[l] = n.chunks;
-        n.chunks += (n.rows[l] + n.chunk_rows - 1) / n.chunk_rows;
+        // (levels that do not share rows hold Nv together at most)
+        if (h * w > d.Nv - n.cum[l])
+            return api_failf(MSDA_ERR_INVALID_ARG, "level %d shares rows with another", l);
+        n.cum[l + 1] = n.cum[l] + (int)(h * w);
         int k = l;  // the levels by their first row
         for (; k > 0 && n.start[order[k - 1]] > n.start[l]; --k) order[k] = order[k - 1];
         order[k] = l;
     }
-    n.chunk0[d.L] = n.chunks;
+    n.used = n.cum[d.L];
     int at = 0;
     for (int k = 0; k <= d.L; ++k) {
         const int start = k < d.L ? n.start[order[k]] : d.Nv;
@@ -673,14 +885,15 @@ msda_status_t norm_shape(const msda_norm_dims_t& d, const int64_t* shapes, const
         if (start > at) {
             n.gap_start[n.gaps] = at;
             n.gap_rows[n.gaps++] = start - at;
-            n.gap_chunks += (start - at + n.chunk_rows - 1) / n.chunk_rows;
         }
-        if (k < d.L) at = start + n.rows[order[k]];
+        if (k < d.L) at = start + n.cum[order[k] + 1] - n.cum[order[k]];
     }
-    // chunks are counted in 32 bits over all items (elements in 64)
-    if ((int64_t)d.B * (n.chunks + n.gap_chunks) > INT32_MAX - (1 << 20) ||
-        (int64_t)d.B * d.L > INT32_MAX)
+    // rows are counted in 48 bits, so that their products with the runs fit 64
+    if ((int64_t)d.B * d.Nv > ((int64_t)1 << 48) || (int64_t)d.B * d.L > INT32_MAX)
         return api_fail(MSDA_ERR_UNSUPPORTED, "too many rows");
+    // four rows per thread at least
+    const int64_t least = (int64_t)n.slots * 4;
+    n.runs = (int)std::min<int64_t>(kMaxRuns, ((int64_t)d.B * n.used + least - 1) / least);
     return MSDA_OK;
 }
 
@@ -725,40 +938,61 @@ msda_status_t norm_dtype(msda_dtype_t t, const char* name)
     return MSDA_OK;
 }
 
-template <bool kX, bool kY, int kAct>
-cudaError_t apply_forward(const void* x, const NormShape& n, const float4* stats,
-                          const float* gamma, const float* beta, void* y, cudaStream_t s)
+struct NormArgs {
+    const void* x;
+    NormShape n;
+    const float *gamma, *beta;
+    float eps;
+    double2* part;
+    double* middle;
+    void* y;
+    float *mean, *rstd;
+};
+
+// Lets a kernel have the ring (above the 48 KB that need no leave), once per
+// device and kernel.
+template <auto kKernel>
+cudaError_t allow_ring()
 {
-    return launch_pdl(norm_apply_kernel<kX, kY, kAct>, dim3(n.B * (n.chunks + n.gap_chunks)),
-                      dim3(kNormThreads), 0, s, x, n, stats, gamma, beta, y);
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
-template <bool kX>
-cudaError_t run_forward(const void* x, const NormShape& n, const float* gamma, const float* beta,
-                        float eps, msda_activation_t act, bool y_bf16, void* y, float* mean,
-                        float* rstd, double2* part, float4* stats, cudaStream_t s)
+template <bool kX, bool kY, int kAct>
+cudaError_t run_forward(const NormArgs& a, cudaStream_t s)
 {
-    norm_stats_kernel<kX><<<n.B * n.chunks, kNormThreads, 0, s>>>(x, n, part);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = allow_ring<norm_stats_kernel<kX>>();
+    if (e == cudaSuccess) e = allow_ring<norm_apply_kernel<kX, kY, kAct>>();
     if (e != cudaSuccess) return e;
-    e = launch_pdl(norm_merge_kernel, dim3(n.B * n.L, (n.G + 31) / 32), dim3(kMergeThreads), 0, s,
-                   part, n, eps, stats, mean, rstd);
+    norm_stats_kernel<kX><<<a.n.runs, kNormThreads, kRingBytes, s>>>(a.x, a.n, a.part,
+                                                                         a.middle);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    auto go = y_bf16 ? apply_forward<kX, true, MSDA_ACT_NONE> : apply_forward<kX, false, MSDA_ACT_NONE>;
-    if (act == MSDA_ACT_RELU)
-        go = y_bf16 ? apply_forward<kX, true, MSDA_ACT_RELU> : apply_forward<kX, false, MSDA_ACT_RELU>;
-    if (act == MSDA_ACT_SILU)
-        go = y_bf16 ? apply_forward<kX, true, MSDA_ACT_SILU> : apply_forward<kX, false, MSDA_ACT_SILU>;
-    return go(x, n, stats, gamma, beta, y, s);
+    return launch_pdl(norm_apply_kernel<kX, kY, kAct>, dim3(a.n.runs), dim3(kNormThreads),
+                      kRingBytes, s, a.x, a.n, a.part, a.middle, a.eps, a.gamma, a.beta, a.y, a.mean, a.rstd);
+}
+
+template <bool kX, bool kY>
+cudaError_t run_forward(const NormArgs& a, msda_activation_t act, cudaStream_t s)
+{
+    if (act == MSDA_ACT_RELU) return run_forward<kX, kY, MSDA_ACT_RELU>(a, s);
+    if (act == MSDA_ACT_SILU) return run_forward<kX, kY, MSDA_ACT_SILU>(a, s);
+    return run_forward<kX, kY, MSDA_ACT_NONE>(a, s);
 }
 
 struct GradArgs {
     const void *x, *dy;
     NormShape n;
     const float *mean, *rstd, *gamma, *beta;
-    float* part;
-    double2* chan;
-    float2* coef;
+    float* chan;
+    double2* part;
     void* dx;
     float *dgamma, *dbeta;
 };
@@ -767,19 +1001,16 @@ template <bool kX, bool kDy, bool kDx, int kAct>
 cudaError_t run_backward(const GradArgs& a, cudaStream_t s)
 {
     const NormShape& n = a.n;
-    norm_grad_sums_kernel<kX, kDy, kAct><<<n.B * n.chunks, kNormThreads, 0, s>>>(
-        a.x, a.dy, n, a.mean, a.rstd, a.gamma, a.beta, a.part);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = allow_ring<norm_grad_sums_kernel<kX, kDy, kAct>>();
+    if (e == cudaSuccess) e = allow_ring<norm_grad_apply_kernel<kX, kDy, kDx, kAct>>();
     if (e != cudaSuccess) return e;
-    const int per_block = n.cg > 32 ? 1 : 32 / n.cg;
-    e = launch_pdl(norm_grad_merge_kernel, dim3(n.B * n.L, (n.G + per_block - 1) / per_block),
-                   dim3(kMergeThreads), 0, s, a.part, n, per_block, a.gamma, a.chan, a.coef);
+    norm_grad_sums_kernel<kX, kDy, kAct><<<n.runs, kNormThreads, kRingBytes, s>>>(
+        a.x, a.dy, n, a.mean, a.rstd, a.gamma, a.beta, a.chan, a.part);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int extra = (n.L * n.C + kNormThreads - 1) / kNormThreads;
     return launch_pdl(norm_grad_apply_kernel<kX, kDy, kDx, kAct>,
-                      dim3(n.B * (n.chunks + n.gap_chunks) + extra), dim3(kNormThreads), 0, s, a.x,
-                      a.dy, n, a.mean, a.rstd, a.gamma, a.beta, a.chan, a.coef, a.dx, a.dgamma,
-                      a.dbeta);
+                      dim3(n.runs + n.L * ((n.C + 31) / 32)), dim3(kNormThreads), kRingBytes, s,
+                      a.x, a.dy, n, a.mean, a.rstd, a.gamma, a.beta, a.chan, a.part, a.dx, a.dgamma, a.dbeta);
 }
 
 template <bool kX, bool kDy, bool kDx>
@@ -798,16 +1029,15 @@ using namespace msda;
 extern "C" size_t msda_group_norm_workspace_size(msda_norm_dims_t d)
 {
     if (!norm_sizes_ok(d)) return 0;
-    return up256(sizeof(double2) * d.B * norm_max_chunks(d) * d.G) +
-           up256(sizeof(float4) * d.B * d.L * (size_t)d.G);
+    return up256(sizeof(double2) * norm_max_spans(d) * d.G) +
+           up256(sizeof(double) * d.B * d.L * (size_t)d.G);
 }
 
 extern "C" size_t msda_group_norm_backward_workspace_size(msda_norm_dims_t d)
 {
     if (!norm_sizes_ok(d)) return 0;
-    return up256(sizeof(float) * 2 * d.B * norm_max_chunks(d) * d.C) +
-           up256(sizeof(double2) * d.B * d.L * (size_t)d.C) +
-           up256(sizeof(float2) * d.B * d.L * (size_t)d.G);
+    return up256(sizeof(double2) * norm_max_spans(d) * d.G) +
+           up256(sizeof(float) * 2 * norm_max_spans(d) * d.C);
 }
 
 extern "C" msda_status_t msda_group_norm(const void* x, msda_dtype_t x_dtype,
@@ -818,8 +1048,8 @@ extern "C" msda_status_t msda_group_norm(const void* x, msda_dtype_t x_dtype,
                                          float* mean, float* rstd, void* workspace,
                                          size_t workspace_bytes, msda_stream_t stream)
 {
-    NormShape n;
-    NORM_TRY(norm_shape(d, spatial_shapes, level_start_index, n));
+    NormArgs a;
+    NORM_TRY(norm_shape(d, spatial_shapes, level_start_index, a.n));
     NORM_TRY(norm_dtype(x_dtype, "x_dtype"));
     NORM_TRY(norm_dtype(y_dtype, "y_dtype"));
     if (act < MSDA_ACT_NONE || act > MSDA_ACT_SILU)
@@ -836,13 +1066,21 @@ extern "C" msda_status_t msda_group_norm(const void* x, msda_dtype_t x_dtype,
     if (overlap(x, tensor_bytes(d, x_dtype), y, tensor_bytes(d, y_dtype)))
         return api_fail(MSDA_ERR_INVALID_ARG, "y overlaps x");
     NORM_TRY(norm_workspace(workspace, workspace_bytes, msda_group_norm_workspace_size(d)));
-    double2* part = static_cast<double2*>(workspace);
-    float4* stats = reinterpret_cast<float4*>(
-        static_cast<char*>(workspace) + up256(sizeof(double2) * d.B * norm_max_chunks(d) * d.G));
-    const auto run = x_dtype == MSDA_BF16 ? run_forward<true> : run_forward<false>;
-    return api_cuda(run(x, n, gamma, beta, eps, act, y_dtype == MSDA_BF16, y, mean, rstd, part,
-                        stats, (cudaStream_t)stream),
-                    "msda_group_norm");
+    a.x = x;
+    a.gamma = gamma;
+    a.beta = beta;
+    a.eps = eps;
+    a.part = static_cast<double2*>(workspace);
+    a.middle = reinterpret_cast<double*>(static_cast<char*>(workspace) +
+                                         up256(sizeof(double2) * norm_max_spans(d) * d.G));
+    a.y = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    const auto run = x_dtype == MSDA_BF16
+                         ? (y_dtype == MSDA_BF16 ? run_forward<true, true> : run_forward<true, false>)
+                         : (y_dtype == MSDA_BF16 ? run_forward<false, true>
+                                                 : run_forward<false, false>);
+    return api_cuda(run(a, act, (cudaStream_t)stream), "msda_group_norm");
 }
 
 extern "C" msda_status_t msda_group_norm_backward(
@@ -889,11 +1127,8 @@ extern "C" msda_status_t msda_group_norm_backward(
     a.rstd = rstd;
     a.gamma = gamma;
     a.beta = beta;
-    a.part = reinterpret_cast<float*>(w);
-    w += up256(sizeof(float) * 2 * d.B * norm_max_chunks(d) * d.C);
-    a.chan = reinterpret_cast<double2*>(w);
-    w += up256(sizeof(double2) * d.B * d.L * (size_t)d.C);
-    a.coef = reinterpret_cast<float2*>(w);
+    a.part = reinterpret_cast<double2*>(w);
+    a.chan = reinterpret_cast<float*>(w + up256(sizeof(double2) * norm_max_spans(d) * d.G));
     a.dx = grad_x;
     a.dgamma = grad_gamma;
     a.dbeta = grad_beta;
