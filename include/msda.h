@@ -29,8 +29,8 @@
  *   - The library allocates no memory and keeps no pointer after returning.
  *     Its only state: a per-thread error message, a per-device cache of the
  *     SM count, the fixed scratch array of sca_compact_no_alloc, the device
- *     counter read by msda_linear_timeouts, and (set once) the GEMM kernel's
- *     shared-memory attribute and the driver's tensor-map encoder.
+ *     counter read by msda_linear_timeouts, and (set once) the shared-memory
+ *     attributes of kernels and the driver's tensor-map encoder.
  *   - Calls are asynchronous on `stream` (NULL = the legacy default stream).
  *     The status covers argument checks and kernel launch errors; errors that
  *     happen while the kernels run surface at the caller's next
@@ -624,7 +624,7 @@ typedef struct {
     const float* tau;      /* [B, Nq, H] fp32 */
     const int32_t* q_group; /* [B, Nq], or NULL (then k_group is NULL) */
     const int32_t* k_group; /* [B, Nk] */
-    float scale;           /* of the products, usually 32^-1/2; finite */
+    float scale;           /* of the products, usually 32^-1/2; 1e-6 .. 1e6 */
     int32_t B, Nq, Nk, H;
 } msda_attention_t;
 
@@ -648,8 +648,8 @@ typedef struct {
  * The products are exact and accumulate in fp32, softmax and sums are fp32;
  * the weights are rounded to bf16 for their product with v.  q, k, v and out
  * 16-byte aligned, points 8-byte; workspace >=
- * msda_query_attention_workspace_size(p) bytes (which looks at B, Nq, Nk and
- * H), 256-byte aligned, contents ignored. */
+ * msda_query_attention_workspace_size(p) bytes (which looks at B, Nq, Nk, H
+ * and whether there is a tau), 256-byte aligned, contents ignored. */
 size_t msda_query_attention_workspace_size(const msda_attention_t* p);
 msda_status_t msda_query_attention(const msda_attention_t* p, void* out, float* lse,
                                    void* workspace, size_t workspace_bytes,

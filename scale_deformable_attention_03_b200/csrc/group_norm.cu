@@ -28,7 +28,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 
 #include "msda.h"
@@ -949,27 +948,11 @@ struct NormArgs {
     float *mean, *rstd;
 };
 
-// Lets a kernel have the ring (above the 48 KB that need no leave), once per
-// device and kernel.
-template <auto kKernel>
-cudaError_t allow_ring()
-{
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
-    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-    return e;
-}
-
 template <bool kX, bool kY, int kAct>
 cudaError_t run_forward(const NormArgs& a, cudaStream_t s)
 {
-    cudaError_t e = allow_ring<norm_stats_kernel<kX>>();
-    if (e == cudaSuccess) e = allow_ring<norm_apply_kernel<kX, kY, kAct>>();
+    cudaError_t e = allow_shared<norm_stats_kernel<kX>>(kRingBytes);
+    if (e == cudaSuccess) e = allow_shared<norm_apply_kernel<kX, kY, kAct>>(kRingBytes);
     if (e != cudaSuccess) return e;
     norm_stats_kernel<kX><<<a.n.runs, kNormThreads, kRingBytes, s>>>(a.x, a.n, a.part,
                                                                          a.middle);
@@ -1001,8 +984,8 @@ template <bool kX, bool kDy, bool kDx, int kAct>
 cudaError_t run_backward(const GradArgs& a, cudaStream_t s)
 {
     const NormShape& n = a.n;
-    cudaError_t e = allow_ring<norm_grad_sums_kernel<kX, kDy, kAct>>();
-    if (e == cudaSuccess) e = allow_ring<norm_grad_apply_kernel<kX, kDy, kDx, kAct>>();
+    cudaError_t e = allow_shared<norm_grad_sums_kernel<kX, kDy, kAct>>(kRingBytes);
+    if (e == cudaSuccess) e = allow_shared<norm_grad_apply_kernel<kX, kDy, kDx, kAct>>(kRingBytes);
     if (e != cudaSuccess) return e;
     norm_grad_sums_kernel<kX, kDy, kAct><<<n.runs, kNormThreads, kRingBytes, s>>>(
         a.x, a.dy, n, a.mean, a.rstd, a.gamma, a.beta, a.chan, a.part);

@@ -4,14 +4,14 @@
 // One pass over the keys with the running maximum and sum of the softmax, in
 // the base-2 logarithm's units.  A CTA takes 64 queries of one or (with the
 // bias) two heads, so that a distance serves both; its keys come in tiles of
-// 64 through a double buffer of asynchronous copies.  Tiles that no query of
-// the CTA sees are skipped, tiles without a masked pair take no comparison.
-// Where the queries do not fill the GPU the keys are split over CTAs, whose
-// sums a second kernel joins.
+// 64 through a ring of asynchronous copies.  Tiles that no query of the CTA
+// sees are skipped, tiles without a masked pair take no comparison.  Where the
+// queries do not fill the GPU evenly the keys are split over CTAs, whose sums a
+// second kernel joins.
 //
-// Bound by the exponentials (one per score) and square roots (one per pair of
-// points and two heads) at 16 per clock and SM, and by the issue of about 14
-// instructions per score.
+// With 32 channels per head the products are not what binds: a score costs 64
+// multiply-adds, but also an exponential, and a square root per pair of points
+// and two heads, at 16 per clock and SM.
 #include <algorithm>
 
 #include "query_attention.cuh"
@@ -22,6 +22,9 @@ namespace {
 
 constexpr int kSms = 148;
 constexpr int kMaxSplits = 64;
+constexpr int kBlocks = 3;  // CTAs per SM: 168 registers a thread
+constexpr int kStages = 3;  // tiles in shared memory
+constexpr int kPart = 32;   // keys per step: scores and distances in registers
 
 struct ForwardArgs {
     Inputs in;
@@ -35,47 +38,32 @@ struct ForwardArgs {
 
 template <int HP>
 struct ForwardSmem {
-    alignas(128) unsigned char k[2][HP * kTileBytes];
-    alignas(128) unsigned char v[2][HP * kTileBytes];
-    float2 pos[2][kTile];
-    int32_t group[2][kTile];
+    alignas(128) unsigned char k[kStages][HP * kTileBytes];
+    alignas(128) unsigned char v[kStages][HP * kTileBytes];
+    Points pos[kStages];
+    int32_t group[kStages][kTile];
     TileBits bits;
 };
 
 template <int HP, bool kBias>
-__device__ __forceinline__ void load_keys(ForwardSmem<HP>& sm, int stage, const Inputs& in, int b,
-                                          int h, int tile)
+__device__ __forceinline__ void load_keys(ForwardSmem<HP>& sm, int stage, const Inputs& in,
+                                          const TileCopy<HP>& copy, int b, int tile)
 {
-    const int r0 = tile * kTile;
-    const uint32_t sk = smem_addr(sm.k[stage]), sv = smem_addr(sm.v[stage]);
-#pragma unroll
-    for (int i = 0; i < 2 * HP; ++i) {
-        const int id = i * kAttnThreads + (int)threadIdx.x;
-        const int c = id % (4 * HP), row = id / (4 * HP);
-        const int64_t key = (int64_t)b * in.Nk + r0 + row;
-        bool on = r0 + row < in.Nk;
-        // what padding rows hold must not meet a weight of zero
-        if (on && in.kg != nullptr) on = __ldg(in.kg + key) >= 0;
-        const uint32_t dst = (c / 4) * kTileBytes + tile_at(row, c % 4);
-        cp_async<16>(sk + dst, on ? in.k + key * in.ldk + h * kDim + c * 8 : in.k, on);
-        cp_async<16>(sv + dst, on ? in.v + key * in.ldv + h * kDim + c * 8 : in.v, on);
-    }
-    if (threadIdx.x < kTile) {
-        const int row = r0 + threadIdx.x;
-        const int64_t key = (int64_t)b * in.Nk + row;
-        const bool on = row < in.Nk;
-        if constexpr (kBias)
-            cp_async<8>(smem_addr(&sm.pos[stage][threadIdx.x]), on ? in.kp + key : in.kp, on);
-        if (in.kg != nullptr)
-            cp_async<4>(smem_addr(&sm.group[stage][threadIdx.x]), on ? in.kg + key : in.kg, on);
-    }
+    const int64_t first = (int64_t)b * in.Nk;
+    // what padding rows hold must not meet a weight of zero
+    const bool all = in.kg == nullptr && tile * kTile + kTile <= in.Nk;
+    copy.fetch(smem_addr(sm.k[stage]), smem_addr(sm.v[stage]), tile, all,
+               [&](int key) { return in.kg == nullptr || __ldg(in.kg + first + key) >= 0; });
+    load_columns<kBias>(sm.pos[stage], sm.group[stage], in.kp, in.kg, first, tile * kTile, in.Nk);
     cp_commit();
 }
 
 template <int HP, bool kBias>
-__global__ void __launch_bounds__(kAttnThreads) attention_forward_kernel(const ForwardArgs a)
+__global__ void __launch_bounds__(kAttnThreads, kBlocks)
+    attention_forward_kernel(const ForwardArgs a)
 {
-    __shared__ ForwardSmem<HP> sm;
+    extern __shared__ __align__(128) unsigned char smem[];
+    ForwardSmem<HP>& sm = *reinterpret_cast<ForwardSmem<HP>*>(smem);
     const Inputs& in = a.in;
     int id = blockIdx.x;
     const int qt = id % a.q_tiles;
@@ -94,175 +82,207 @@ __global__ void __launch_bounds__(kAttnThreads) attention_forward_kernel(const F
     for (int hh = 0; hh < HP; ++hh)
         load_rows(qf[hh], in.q + (int64_t)b * in.Nq * in.ldq + (h + hh) * kDim, in.ldq, row, on0,
                   on1, t);
-    float2 p0{}, p1{};
-    float tau0[HP] = {}, tau1[HP] = {};
+    // Scores are kept in units of the products q . k, and tau in the same units:
+    // one multiply-add adds the bias, another takes the reference off and
+    // changes to the base-2 logarithm.
+    const float unit = in.scale * kLog2e;
+    float2 p[2] = {};
+    float tau[HP][2] = {};
     if constexpr (kBias) {
-        if (on0) p0 = __ldg(in.qp + q0);
-        if (on1) p1 = __ldg(in.qp + q0 + 8);
 #pragma unroll
-        for (int hh = 0; hh < HP; ++hh) {
-            if (on0) tau0[hh] = __ldg(in.tau + q0 * in.H + h + hh) * kLog2e;
-            if (on1) tau1[hh] = __ldg(in.tau + (q0 + 8) * in.H + h + hh) * kLog2e;
+        for (int half = 0; half < 2; ++half) {
+            if (!(half ? on1 : on0)) continue;
+            const float2 at = __ldg(in.qp + q0 + 8 * half);
+            p[half] = make_float2(-at.x, -at.y);
+#pragma unroll
+            for (int hh = 0; hh < HP; ++hh)
+                tau[hh][half] = -__ldg(in.tau + (q0 + 8 * half) * in.H + h + hh) / in.scale;
         }
     }
     int g0 = 0, g1 = 0;
-    GroupRange own{0, 0, true, true, true};
+    GroupRange own{0, 0, true, true, true, true};
     if (in.qg != nullptr) {
         g0 = on0 ? __ldg(in.qg + q0) : -1;
         g1 = on1 ? __ldg(in.qg + q0 + 8) : -1;
         own = warp_range(in.qg, (int64_t)b * in.Nq + qt * kRows, min(kRows, in.Nq - qt * kRows));
     }
-    const float scale = in.scale * kLog2e;
-
-    float o[HP][4][4] = {}, m0[HP], m1[HP], l0[HP] = {}, l1[HP] = {};
+    // The reference that is taken off stays the same until a score is 2^kSlack
+    // times above it: weights up to 2^kSlack are as exact as weights up to 1, and
+    // after the first tiles nothing has to be scaled again.
+    constexpr float kSlack = 8.0f;
+    const float slack = kSlack / unit;
+    float o[HP][4][4] = {}, m[HP][2], base[HP][2] = {};
+    float2 l[HP][2] = {};
 #pragma unroll
-    for (int hh = 0; hh < HP; ++hh) m0[hh] = m1[hh] = -INFINITY;
+    for (int hh = 0; hh < HP; ++hh) m[hh][0] = m[hh][1] = -INFINITY;
 
+    const LaneAt lanes = lane_at(lane);
+    const TileCopy<HP> copy(in.k + (int64_t)b * in.Nk * in.ldk + h * kDim, in.ldk,
+                            in.v + (int64_t)b * in.Nk * in.ldv + h * kDim, in.ldv, in.Nk);
     const int tiles = (in.Nk + kTile - 1) / kTile;
     const int begin = split * a.split_tiles, last = min(tiles, begin + a.split_tiles);
     for (int first = begin; first < last; first += kScan) {
+        __syncthreads();  // the bits of the tiles before are read
         scan_tiles<false>(sm.bits, own, true, in.kg, (int64_t)b * in.Nk, in.Nk, first, last);
         int tile = next_tile(sm.bits, first, first, last), stage = 0;
-        if (tile < last) load_keys<HP, kBias>(sm, stage, in, b, h, tile);
+        if (tile >= last) continue;
+        load_keys<HP, kBias>(sm, 0, in, copy, b, tile);
+        cp_wait<0>();
+        __syncthreads();
+        int ahead = next_tile(sm.bits, tile + 1, first, last);
+        if (ahead < last) load_keys<HP, kBias>(sm, 1, in, copy, b, ahead);
+
+        // A step is 32 keys of a head.  Its products are asked for one step early,
+        // so that the matrix pipe works while the weights of the step before are
+        // formed; the step after a tile's last is the next tile's first.
+        float c[4][4];      // products of the next step
+        float2 dist[4][2];  // distances of the next step's keys
+        float2 s[4][2];     // scores, then weights, of this one
+        const auto products = [&](int st, int part, int hh) {
+            const uint32_t sk = smem_addr(sm.k[st]) + hh * kTileBytes;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t r[4];
+                load_cols(r, sk, 4 * part + j, lanes);
+                mma_first(c[j], qf[hh], r[0], r[1]);
+                mma(c[j], qf[hh] + 4, r[2], r[3]);
+            }
+            if (kBias && hh == 0) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int at = kPart * part + 8 * j + 2 * t;
+                    const float2 x = *reinterpret_cast<const float2*>(&sm.pos[st].x[at]);
+                    const float2 y = *reinterpret_cast<const float2*>(&sm.pos[st].y[at]);
+                    dist[j][0] = distances(p[0].x, p[0].y, x, y);
+                    dist[j][1] = distances(p[1].x, p[1].y, x, y);
+                }
+            }
+        };
+        // Scores from the products, and their row's reference.
+        const auto scores = [&](int st, int part, int hh, int of_tile) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    s[j][half] = pair(c[j], half);
+                    if constexpr (kBias)
+                        s[j][half] = __ffma2_rn(dist[j][half], both(tau[hh][half]), s[j][half]);
+                }
+            }
+            const int bit = of_tile - first;
+            if (!((sm.bits.clear[bit >> 5] >> (bit & 31)) & 1)) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int at = kPart * part + 8 * j + 2 * t;
+                    const int key = of_tile * kTile + at;
+                    int2 kg = make_int2(0, 0);
+                    if (in.kg != nullptr) kg = *reinterpret_cast<const int2*>(&sm.group[st][at]);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int qg = half ? g1 : g0;
+                        if (key >= in.Nk || !sees(qg, kg.x)) s[j][half].x = -INFINITY;
+                        if (key + 1 >= in.Nk || !sees(qg, kg.y)) s[j][half].y = -INFINITY;
+                    }
+                }
+            }
+            float top[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                top[half] = fmaxf(s[0][half].x, s[0][half].y);
+#pragma unroll
+                for (int j = 1; j < 4; ++j) top[half] = max3(top[half], s[j][half].x, s[j][half].y);
+            }
+            if (__any_sync(0xffffffffu,
+                           top[0] > m[hh][0] + slack || top[1] > m[hh][1] + slack)) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float n = top[half];
+                    n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 1));
+                    n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 2));
+                    n = fmaxf(n, m[hh][half]);
+                    // (a row that has seen nothing has nothing to scale)
+                    const float f =
+                        m[hh][half] == -INFINITY ? 0.0f : exp2_approx((m[hh][half] - n) * unit);
+                    m[hh][half] = n;
+                    base[hh][half] = n == -INFINITY ? 0.0f : n * unit;
+                    l[hh][half] = __fmul2_rn(l[hh][half], both(f));
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        o[hh][d][2 * half] *= f;
+                        o[hh][d][2 * half + 1] *= f;
+                    }
+                }
+            }
+        };
+        products(0, 0, 0);
+        scores(0, 0, 0, tile);
         while (tile < last) {
-            const int ahead = next_tile(sm.bits, tile + 1, first, last);
-            if (ahead < last) {
-                load_keys<HP, kBias>(sm, stage ^ 1, in, b, h, ahead);
-                cp_wait<1>();
-            } else {
-                cp_wait<0>();
-            }
-            __syncthreads();
-            const bool clear = (sm.bits.clear[(tile - first) >> 5] >> ((tile - first) & 31)) & 1;
-            float dist[8][4];
-            if constexpr (kBias) {
+            const int next = stage == kStages - 1 ? 0 : stage + 1;
+            const int after = ahead < last ? next_tile(sm.bits, ahead + 1, first, last) : last;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float4 pk =
-                        *reinterpret_cast<const float4*>(&sm.pos[stage][8 * j + 2 * t]);
-                    dist[j][0] = distance(p0, pk.x, pk.y);
-                    dist[j][1] = distance(p0, pk.z, pk.w);
-                    dist[j][2] = distance(p1, pk.x, pk.y);
-                    dist[j][3] = distance(p1, pk.z, pk.w);
+            for (int u = 0; u < HP * (kTile / kPart); ++u) {
+                const int part = u / HP, hh = u % HP;
+                const bool ends = u + 1 == HP * (kTile / kPart);
+                if (ends) {
+                    cp_wait<0>();     // the next tile is here, and
+                    __syncthreads();  // nobody reads the one before this any more
+                    if (after < last)
+                        load_keys<HP, kBias>(sm, next == kStages - 1 ? 0 : next + 1, in, copy, b,
+                                             after);
+                    products(next, 0, 0);  // (of no use behind the last tile)
+                } else {
+                    products(stage, (u + 1) / HP, (u + 1) % HP);
                 }
-            }
-            uint32_t hide = 0;  // pairs of this thread that are masked
-            if (!clear) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int half = 0; half < 2; ++half) {
+                    float2 sum = both(0.0f);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int at = 8 * j + 2 * t + c;
-                        const bool in_range = tile * kTile + at < in.Nk;
-                        const int kg = in.kg != nullptr ? sm.group[stage][at] : 0;
-                        hide |= (uint32_t)!(in_range && sees(g0, kg)) << (4 * j + c);
-                        hide |= (uint32_t)!(in_range && sees(g1, kg)) << (4 * j + 2 + c);
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 x = __ffma2_rn(s[j][half], both(unit), both(-base[hh][half]));
+                        s[j][half] = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                        sum = __fadd2_rn(sum, s[j][half]);
                     }
+                    l[hh][half] = __fadd2_rn(l[hh][half], sum);
                 }
-            }
-#pragma unroll
-            for (int hh = 0; hh < HP; ++hh) {
-                const uint32_t sk = smem_addr(sm.k[stage]) + hh * kTileBytes;
                 const uint32_t sv = smem_addr(sm.v[stage]) + hh * kTileBytes;
-                float s[8][4] = {};
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    uint32_t r[4];
-                    load_cols(r, sk, j, lane);
-                    mma(s[j], qf[hh], r[0], r[1]);
-                    mma(s[j], qf[hh] + 4, r[2], r[3]);
-                }
-                float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        s[j][c] *= scale;
-                        if constexpr (kBias)
-                            s[j][c] = fmaf(c < 2 ? -tau0[hh] : -tau1[hh], dist[j][c], s[j][c]);
-                    }
-                }
-                if (!clear) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if ((hide >> (4 * j + c)) & 1) s[j][c] = -INFINITY;
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    t0 = fmaxf(t0, fmaxf(s[j][0], s[j][1]));
-                    t1 = fmaxf(t1, fmaxf(s[j][2], s[j][3]));
-                }
-                t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
-                t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
-                t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
-                t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
-                const float n0 = fmaxf(m0[hh], t0), n1 = fmaxf(m1[hh], t1);
-                // a row that has seen nothing yet stays at weight zero
-                const float b0 = n0 == -INFINITY ? 0.0f : n0, b1 = n1 == -INFINITY ? 0.0f : n1;
-                const float f0 = exp2_approx(m0[hh] - b0), f1 = exp2_approx(m1[hh] - b1);
-                m0[hh] = n0;
-                m1[hh] = n1;
-                float a0 = 0.0f, a1 = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    s[j][0] = exp2_approx(s[j][0] - b0);
-                    s[j][1] = exp2_approx(s[j][1] - b0);
-                    s[j][2] = exp2_approx(s[j][2] - b1);
-                    s[j][3] = exp2_approx(s[j][3] - b1);
-                    a0 += s[j][0] + s[j][1];
-                    a1 += s[j][2] + s[j][3];
-                }
-                l0[hh] = fmaf(l0[hh], f0, a0);
-                l1[hh] = fmaf(l1[hh], f1, a1);
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    o[hh][d][0] *= f0;
-                    o[hh][d][1] *= f0;
-                    o[hh][d][2] *= f1;
-                    o[hh][d][3] *= f1;
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 2; ++k) {
                     // the weights in bf16: the matrix instruction's type, v's own; 2^-8 of
                     // each at most, what out's own rounding may be
-                    const uint32_t pf[4] = {pack_bf16(s[2 * k][0], s[2 * k][1]),
-                                            pack_bf16(s[2 * k][2], s[2 * k][3]),
-                                            pack_bf16(s[2 * k + 1][0], s[2 * k + 1][1]),
-                                            pack_bf16(s[2 * k + 1][2], s[2 * k + 1][3])};
+                    const uint32_t pf[4] = {pack_bf16(s[2 * k][0]), pack_bf16(s[2 * k][1]),
+                                            pack_bf16(s[2 * k + 1][0]),
+                                            pack_bf16(s[2 * k + 1][1])};
 #pragma unroll
-                    for (int d = 0; d < 4; d += 2) {
+                    for (int d = 0; d < 2; ++d) {
                         uint32_t r[4];
-                        load_sum(r, sv, k, d, lane);
-                        mma(o[hh][d], pf, r[0], r[1]);
-                        mma(o[hh][d + 1], pf, r[2], r[3]);
+                        load_sum(r, sv, 2 * part + k, d, lanes);
+                        mma(o[hh][2 * d], pf, r[0], r[1]);
+                        mma(o[hh][2 * d + 1], pf, r[2], r[3]);
                     }
                 }
+                if (!ends) scores(stage, (u + 1) / HP, (u + 1) % HP, tile);
+                else if (ahead < last) scores(next, 0, 0, ahead);
             }
-            __syncthreads();
             tile = ahead;
-            stage ^= 1;
+            ahead = after;
+            stage = next;
         }
     }
 
 #pragma unroll
     for (int hh = 0; hh < HP; ++hh) {
 #pragma unroll
-        for (int x = 1; x < 4; x <<= 1) {
-            l0[hh] += __shfl_xor_sync(0xffffffffu, l0[hh], x);
-            l1[hh] += __shfl_xor_sync(0xffffffffu, l1[hh], x);
-        }
-#pragma unroll
         for (int half = 0; half < 2; ++half) {
+            float sum = l[hh][half].x + l[hh][half].y;
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             if (!(half ? on1 : on0)) continue;
             const int q = row + 8 * half;
-            const float l = half ? l1[hh] : l0[hh], m = half ? m1[hh] : m0[hh];
             // a padding query saw the keys of group 0: it is left out here
-            const bool dead = l == 0.0f || (half ? g1 : g0) < 0;
+            const bool dead = sum == 0.0f || (half ? g1 : g0) < 0;
             const int64_t bhq = ((int64_t)b * in.H + h + hh) * in.Nq + q;
             if (a.splits == 1) {
-                const float w = dead ? 0.0f : 1.0f / l;
+                const float w = dead ? 0.0f : 1.0f / sum;
                 uint32_t* dst = reinterpret_cast<uint32_t*>(
                     a.out + (((int64_t)b * in.Nq + q) * in.H + h + hh) * kDim);
 #pragma unroll
@@ -270,14 +290,16 @@ __global__ void __launch_bounds__(kAttnThreads) attention_forward_kernel(const F
                     dst[4 * d + t] = dead ? 0u : pack_bf16(o[hh][d][2 * half] * w,
                                                            o[hh][d][2 * half + 1] * w);
                 if (a.lse != nullptr && t == 0)
-                    a.lse[bhq] = dead ? -INFINITY : (m + log2f(l)) * kLn2;
+                    a.lse[bhq] = dead ? -INFINITY : (base[hh][half] + log2f(sum)) * kLn2;
             } else {
                 const int64_t at = (int64_t)split * in.B * in.H * in.Nq + bhq;
                 float2* dst = reinterpret_cast<float2*>(a.part + at * kDim);
 #pragma unroll
                 for (int d = 0; d < 4; ++d)
                     dst[4 * d + t] = make_float2(o[hh][d][2 * half], o[hh][d][2 * half + 1]);
-                if (t == 0) a.part_ml[at] = dead ? make_float2(-INFINITY, 0.0f) : make_float2(m, l);
+                if (t == 0)
+                    a.part_ml[at] = dead ? make_float2(-INFINITY, 0.0f)
+                                         : make_float2(base[hh][half], sum);
             }
         }
     }
@@ -317,24 +339,50 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const ForwardArgs a
 }
 
 struct Plan {
-    int q_tiles, splits, split_tiles;
+    int q_tiles, splits, split_tiles, heads;  // heads per CTA
 };
 
-// Two CTAs per SM keep it busy; below that the keys are split, down to two
-// tiles per CTA (a join costs about what two tiles do).
-Plan plan_of(int B, int Nq, int Nk, int H)
+// Two heads per CTA share the distances, where that still fills the GPU (below
+// it more and shorter CTAs are faster).  The keys are split until the CTAs fill
+// one wave, down to two tiles per CTA (a join costs about what two tiles do),
+// and beyond that where it evens out the last wave: 628 CTAs in waves of 444
+// take two of them, halved they take three half as long.
+Plan plan_of(int B, int Nq, int Nk, int H, bool bias)
 {
     Plan p;
     p.q_tiles = (Nq + kRows - 1) / kRows;
-    const int64_t ctas = (int64_t)p.q_tiles * B * H;
+    const int64_t wave = kBlocks * kSms;
     const int tiles = (Nk + kTile - 1) / kTile;
-    p.splits = 1;
-    if (ctas < 2 * kSms)
-        p.splits = (int)std::max<int64_t>(
-            1, std::min<int64_t>({(2 * kSms + ctas - 1) / ctas, (tiles + 1) / 2, kMaxSplits}));
-    p.split_tiles = std::max(1, (tiles + p.splits - 1) / p.splits);
+    int64_t ctas = (int64_t)p.q_tiles * B * H;
+    p.heads = bias && H % 2 == 0 && ctas >= 2 * wave ? 2 : 1;
+    ctas /= p.heads;
+    int64_t splits = wave / std::max<int64_t>(ctas, 1);
+    if (splits <= 1) {
+        // waves in units of a whole one, 2 % of a wave for each split's join
+        double least = 1e30;
+        for (int s = 1; s <= 4; ++s) {
+            const double cost = (double)((ctas * s + wave - 1) / wave) / s + 0.02 * (s - 1);
+            if (cost < least) {
+                least = cost;
+                splits = s;
+            }
+        }
+    }
+    splits = std::max<int64_t>(1, std::min<int64_t>({splits, (tiles + 1) / 2, kMaxSplits}));
+    p.split_tiles = std::max<int>(1, (tiles + (int)splits - 1) / (int)splits);
     p.splits = std::max(1, (tiles + p.split_tiles - 1) / p.split_tiles);
     return p;
+}
+
+template <int HP, bool kBias>
+cudaError_t run(const ForwardArgs& a, cudaStream_t s)
+{
+    const cudaError_t e = allow_shared<attention_forward_kernel<HP, kBias>>(sizeof(ForwardSmem<HP>));
+    if (e != cudaSuccess) return e;
+    const int64_t ctas = (int64_t)a.q_tiles * a.in.B * (a.in.H / HP) * a.splits;
+    attention_forward_kernel<HP, kBias>
+        <<<(unsigned)ctas, kAttnThreads, sizeof(ForwardSmem<HP>), s>>>(a);
+    return cudaGetLastError();
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -371,8 +419,9 @@ msda_status_t check_inputs(const msda_attention_t* p, bool& empty)
         return api_failf(MSDA_ERR_INVALID_ARG,
                          "B (%d), Nq (%d) and Nk (%d) must be >= 0 and H (%d) >= 1", p->B, p->Nq,
                          p->Nk, p->H);
-    if (!std::isfinite(p->scale))
-        return api_failf(MSDA_ERR_INVALID_ARG, "scale = %g must be finite", (double)p->scale);
+    if (!(p->scale >= 1e-6f && p->scale <= 1e6f))
+        return api_failf(MSDA_ERR_INVALID_ARG, "scale = %g is outside 1e-6 .. 1e6",
+                         (double)p->scale);
     if (p->H > (1 << 20))
         return api_failf(MSDA_ERR_UNSUPPORTED, "H = %d is above 2^20", p->H);
     // CTAs are counted in 32 bits (rows and elements in 64)
@@ -443,7 +492,7 @@ using namespace msda::attn;
 extern "C" size_t msda_query_attention_workspace_size(const msda_attention_t* p)
 {
     if (p == nullptr || p->B <= 0 || p->Nq <= 0 || p->Nk <= 0 || p->H < 1) return 0;
-    const Plan plan = plan_of(p->B, p->Nq, p->Nk, p->H);
+    const Plan plan = plan_of(p->B, p->Nq, p->Nk, p->H, p->tau != nullptr);
     if (plan.splits == 1) return 0;
     const size_t rows = (size_t)plan.splits * p->B * p->H * p->Nq;
     return up256(rows * kDim * sizeof(float)) + up256(rows * sizeof(float2));
@@ -472,7 +521,7 @@ extern "C" msda_status_t msda_query_attention(const msda_attention_t* p, void* o
     a.in = inputs_of(*p);
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;
-    const Plan plan = plan_of(p->B, p->Nq, p->Nk, p->H);
+    const Plan plan = plan_of(p->B, p->Nq, p->Nk, p->H, p->tau != nullptr);
     a.q_tiles = plan.q_tiles;
     a.splits = plan.splits;
     a.split_tiles = plan.split_tiles;
@@ -480,18 +529,9 @@ extern "C" msda_status_t msda_query_attention(const msda_attention_t* p, void* o
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) +
                                           up256(rows * kDim * sizeof(float)));
-    const bool bias = p->tau != nullptr;
-    const int64_t ctas = (int64_t)plan.q_tiles * p->B * p->H * plan.splits;
-    // two heads per CTA share the distances, where that still fills the GPU
-    const bool pair = bias && p->H % 2 == 0 && ctas >= 8 * kSms;
-    cudaError_t e;
-    if (pair)
-        attention_forward_kernel<2, true><<<(unsigned)(ctas / 2), kAttnThreads, 0, s>>>(a);
-    else if (bias)
-        attention_forward_kernel<1, true><<<(unsigned)ctas, kAttnThreads, 0, s>>>(a);
-    else
-        attention_forward_kernel<1, false><<<(unsigned)ctas, kAttnThreads, 0, s>>>(a);
-    e = cudaGetLastError();
+    cudaError_t e = plan.heads == 2 ? run<2, true>(a, s)
+                    : p->tau        ? run<1, true>(a, s)
+                                    : run<1, false>(a, s);
     if (e == cudaSuccess && plan.splits > 1) {
         const int64_t n = (int64_t)p->B * p->H * p->Nq;
         e = launch_pdl(attention_join_kernel, dim3((unsigned)((n * 8 + 255) / 256)), dim3(256), 0,

@@ -45,6 +45,27 @@ __device__ __forceinline__ float sqrt_approx(float x)
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Two neighbouring scores of a row go through the packed fp32 instructions:
+// one issue slot for both.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 pair(const float (&c)[4], int half)
+{
+    return make_float2(c[2 * half], c[2 * half + 1]);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float2 v)
+{
+    const __nv_bfloat162 h = __float22bfloat162_rn(v);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -54,11 +75,19 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 // c += a b for a 16 x 16 by 16 x 8 product.
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t* a, uint32_t b0, uint32_t b1)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The same from zero (no registers to clear).
+__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t* a, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr)
@@ -113,20 +142,80 @@ __device__ __forceinline__ uint32_t tile_at(int row, int chunk)
 
 constexpr int kTileBytes = kTile * 64;  // of one head
 
+// Where a lane's rows of a fragment load start; rows 8 (16) further on are at
+// plain offsets, since the places repeat every eight rows.
+struct LaneAt {
+    uint32_t cols;     // rows lane & 7, chunk lane >> 3
+    uint32_t sum[2];   // rows lane & 15, chunks lane >> 4 and two further on
+};
+
+__device__ __forceinline__ LaneAt lane_at(int lane)
+{
+    return {tile_at(lane & 7, lane >> 3),
+            {tile_at(lane & 15, lane >> 4), tile_at(lane & 15, 2 + (lane >> 4))}};
+}
+
 // B fragments of the product with a tile's rows as columns (scores): all 32
 // channels of the rows 8j .. 8j + 7; r[0], r[1] for channels 0..15, r[2], r[3]
 // for 16..31.
-__device__ __forceinline__ void load_cols(uint32_t (&r)[4], uint32_t tile, int j, int lane)
+__device__ __forceinline__ void load_cols(uint32_t (&r)[4], uint32_t tile, int j, const LaneAt& at)
 {
-    ldsm(r, tile + tile_at(8 * j + (lane & 7), lane >> 3));
+    ldsm(r, tile + at.cols + 512 * j);
 }
 
 // B fragments of the product that sums over a tile's rows 16k .. 16k + 15:
-// r[0], r[1] for channels 8d .. 8d + 7, r[2], r[3] for the eight after them.
-__device__ __forceinline__ void load_sum(uint32_t (&r)[4], uint32_t tile, int k, int d, int lane)
+// r[0], r[1] for channels 16d .. 16d + 7, r[2], r[3] for the eight after them.
+__device__ __forceinline__ void load_sum(uint32_t (&r)[4], uint32_t tile, int k, int d,
+                                         const LaneAt& at)
 {
-    ldsm_t(r, tile + tile_at(16 * k + (lane & 15), d + (lane >> 4)));
+    ldsm_t(r, tile + at.sum[d] + 1024 * k);
 }
+
+// Copies tiles of 64 rows of HP heads of two tensors (keys and values, or
+// queries and their output's gradient) into shared memory.  A thread copies the
+// 16-byte chunk `c` of the rows row, row + kStep, ...; only the start of a tile
+// is computed anew.
+template <int HP>
+struct TileCopy {
+    static constexpr int kChunks = 4 * HP, kStep = kAttnThreads / kChunks;
+    const char *a, *b;        // this thread's chunk of the item's row `row`
+    int64_t lda, ldb;         // bytes from row to row
+    uint32_t to;              // its place in a stage
+    int row, n;               // first row of a tile, rows of the item
+
+    __device__ __forceinline__ TileCopy(const __nv_bfloat16* pa, int64_t la,
+                                        const __nv_bfloat16* pb, int64_t lb, int rows)
+    {
+        const int c = threadIdx.x % kChunks;
+        row = threadIdx.x / kChunks;
+        n = rows;
+        lda = 2 * la;
+        ldb = 2 * lb;
+        a = reinterpret_cast<const char*>(pa) + row * lda + c * 16;
+        b = reinterpret_cast<const char*>(pb) + row * ldb + c * 16;
+        to = (c / 4) * kTileBytes + tile_at(row, c % 4);
+    }
+
+    // on(row): whether the row holds something; others are filled with zeros.
+    template <typename F>
+    __device__ __forceinline__ void fetch(uint32_t sa, uint32_t sb, int tile, bool all, F on) const
+    {
+        const int64_t r0 = (int64_t)tile * kTile;
+        const char *pa = a + r0 * lda, *pb = b + r0 * ldb;
+        // (the places of a chunk repeat every eight rows, and kStep is a multiple of that)
+        static_assert(kStep % 8 == 0, "");
+#pragma unroll
+        for (int i = 0; i < kTile / kStep; ++i) {
+            const uint32_t at = to + i * kStep * 64;
+            bool there = true;
+            if (!all) there = tile * kTile + row + i * kStep < n && on(tile * kTile + row + i * kStep);
+            cp_async<16>(sa + at, there ? pa : a - row * lda, there);
+            cp_async<16>(sb + at, there ? pb : b - row * ldb, there);
+            pa += kStep * lda;
+            pb += kStep * ldb;
+        }
+    }
+};
 
 // A fragments of a warp's 16 rows of one head, straight from memory; a row
 // that is not `on` reads as zero.
@@ -144,17 +233,16 @@ __device__ __forceinline__ void load_rows(uint32_t (&f)[8], const __nv_bfloat16*
     }
 }
 
-// The groups on one side, as far as visibility goes: the range of those >= 0,
-// whether 0 is among them, and whether all are 0.
+// The groups on one side, as far as visibility goes; lo and hi: of those >= 0.
 struct GroupRange {
     int lo, hi;
-    bool any, zero, all_zero;
+    bool any, zero, all_zero, none_below;  // some >= 0, some 0, all 0, none negative
 };
 
 __device__ __forceinline__ GroupRange warp_range(const int32_t* g, int64_t at, int count)
 {
     int lo = INT32_MAX, hi = -1;
-    bool zero = false, all = true;
+    bool zero = false, all = true, below = false;
     for (int i = threadIdx.x & 31; i < count; i += 32) {
         const int v = __ldg(g + at + i);
         if (v >= 0) {
@@ -163,11 +251,12 @@ __device__ __forceinline__ GroupRange warp_range(const int32_t* g, int64_t at, i
         }
         zero |= v == 0;
         all &= v == 0;
+        below |= v < 0;
     }
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
     return {lo, hi, hi >= 0, (bool)__any_sync(0xffffffffu, zero),
-            (bool)__all_sync(0xffffffffu, all)};
+            (bool)__all_sync(0xffffffffu, all), !__any_sync(0xffffffffu, below)};
 }
 
 // Tiles of the other side that some row of the own side needs (bit set in
@@ -177,25 +266,23 @@ struct TileBits {
     uint32_t need[kScan / 32], clear[kScan / 32];
 };
 
-template <bool kOwnKeys>
+template <bool kOwnKeys, int kScanThreads = kAttnThreads, int kRows = kTile>
 __device__ void scan_tiles(TileBits& bits, const GroupRange& own, bool own_full,
                            const int32_t* other, int64_t at, int n, int first, int last)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int w = threadIdx.x; w < kScan / 32; w += kAttnThreads) bits.need[w] = bits.clear[w] = 0;
+    for (int w = threadIdx.x; w < kScan / 32; w += kScanThreads) bits.need[w] = bits.clear[w] = 0;
     __syncthreads();
-    for (int tile = first + warp; tile < min(last, first + kScan); tile += kAttnWarps) {
-        const int r0 = tile * kTile, count = min(kTile, n - r0);
-        bool need = true, clear = count == kTile;
+    for (int tile = first + warp; tile < min(last, first + kScan);
+         tile += kScanThreads / 32) {
+        const int r0 = tile * kRows, count = min(kRows, n - r0);
+        bool need = true, clear = count == kRows;
         if (other != nullptr) {
             const GroupRange g = warp_range(other, at + r0, count);
             const bool meet = g.any && own.any && g.lo <= own.hi && own.lo <= g.hi;
             if constexpr (kOwnKeys) {
                 need = meet || (own.zero && g.any);
-                clear = clear && own_full && own.all_zero && g.any &&
-                        __all_sync(0xffffffffu, __ldg(other + at + r0 + min(lane, count - 1)) >= 0 &&
-                                                    __ldg(other + at + r0 +
-                                                          min(lane + 32, count - 1)) >= 0);
+                clear = clear && own_full && own.all_zero && g.none_below;
             } else {
                 need = own.any && (meet || g.zero);
                 clear = clear && g.all_zero;
@@ -233,10 +320,34 @@ __device__ __forceinline__ bool sees(int q_group, int k_group)
     return q_group >= 0 && k_group >= 0 && (k_group == 0 || k_group == q_group);
 }
 
-__device__ __forceinline__ float distance(float2 a, float x, float y)
+// Distances of a row's point (given negated, nx and ny) from two points.
+__device__ __forceinline__ float2 distances(float nx, float ny, float2 x, float2 y)
 {
-    const float dx = a.x - x, dy = a.y - y;
-    return sqrt_approx(fmaf(dx, dx, dy * dy));
+    const float2 dx = __fadd2_rn(x, both(nx)), dy = __fadd2_rn(y, both(ny));
+    const float2 d = __ffma2_rn(dx, dx, __fmul2_rn(dy, dy));
+    return make_float2(sqrt_approx(d.x), sqrt_approx(d.y));
+}
+
+// The points of a tile, x and y apart so that two neighbours load as a pair.
+struct Points {
+    float x[kTile], y[kTile];
+};
+
+// The points and groups of the tile's rows r0 .. r0 + 63 of an item.
+template <bool kBias>
+__device__ __forceinline__ void load_columns(Points& pos, int32_t* group, const float2* points,
+                                             const int32_t* groups, int64_t first, int r0, int n)
+{
+    if (threadIdx.x >= kTile) return;
+    const int row = r0 + (int)threadIdx.x;
+    const bool on = row < n;
+    if constexpr (kBias) {
+        const float2* src = on ? points + first + row : points;
+        cp_async<4>(smem_addr(&pos.x[threadIdx.x]), &src->x, on);
+        cp_async<4>(smem_addr(&pos.y[threadIdx.x]), &src->y, on);
+    }
+    if (groups != nullptr)
+        cp_async<4>(smem_addr(group + threadIdx.x), on ? groups + first + row : groups, on);
 }
 
 // Device copy of the inputs.

@@ -2,16 +2,16 @@
 // dp_ij = do_i . v_j, D_i = sum_j p_ij dp_ij and ds_ij = p_ij (dp_ij - D_i):
 //   dq_i = scale sum_j ds_ij k_j,  dtau_i = -sum_j ds_ij |p_i - p_j|
 //   dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij do_i
-// Two kernels, one per side, so that every sum has one owner and no atomic is
-// needed.  The queries' kernel walks the keys twice: first for D, then for dq
-// and dtau.  D is formed from the same p and dp that ds uses (not from the
-// rounded output of the forward): ds is then exact where one key takes all the
-// weight, and dtau, an fp32 sum of it, keeps fp32's precision.  It leaves
-// (lse, tau, D) per head and query for the keys' kernel, which walks the
-// queries once.
+// Every sum has one owner, so no atomic is needed.  A first kernel walks the
+// keys for D (its sums joined by a second where the keys are split), the last
+// has two kinds of CTAs, which run side by side so that neither leaves the GPU
+// half empty at its end: 64 queries and all keys for dq and dtau, 64 keys and
+// all queries for dk and dv.  D is formed from the same p and dp that ds uses
+// (not from the rounded output of the forward): ds is then exact where one key
+// takes all the weight, and dtau, an fp32 sum of it, keeps fp32's precision.
 //
 // Bound like the forward by instruction issue and the exponentials (three per
-// pair, and three square roots per pair of points and CTA).
+// pair, and two and a half square roots per pair of points and head).
 #include <algorithm>
 
 #include "query_attention.cuh"
@@ -20,6 +20,9 @@ namespace msda {
 namespace attn {
 namespace {
 
+constexpr int kSms = 148;
+constexpr int kBlocks = 3;  // CTAs per SM: 168 registers a thread
+constexpr int kMaxSplits = 32;
 constexpr int kHalf = 32;  // columns per step: scores, dp and distances in registers
 
 struct BackwardArgs {
@@ -28,46 +31,30 @@ struct BackwardArgs {
     const float* lse;
     __nv_bfloat16 *dq, *dk, *dv;
     float* dtau;
-    float4* rows;  // [B, H, Nq]: lse and tau in units of log 2, D
-    int q_tiles, k_tiles;
+    float* rows;  // [3, B, H, Nq]: -lse and -tau in units of log 2, D
+    float* part;  // [splits, B, H, Nq]: D's sums where the keys are split
+    int q_tiles, k_tiles, splits, split_tiles;
 };
 
 template <int HP>
 struct BackwardSmem {
     alignas(128) unsigned char a[2][HP * kTileBytes];  // keys, or queries
     alignas(128) unsigned char b[2][HP * kTileBytes];  // values, or the output's gradient
-    float4 rows[2][HP][kTile];                         // of the queries (keys' kernel)
-    float2 pos[2][kTile];
+    float rows[2][HP][3][kTile];  // of the queries (keys' kernel): lse, tau, D
+    Points pos[2];
     int32_t group[2][kTile];
     TileBits bits;
 };
 
 template <int HP, bool kBias>
-__device__ __forceinline__ void load_keys(BackwardSmem<HP>& sm, int stage, const Inputs& in, int b,
-                                          int h, int tile)
+__device__ __forceinline__ void load_keys(BackwardSmem<HP>& sm, int stage, const Inputs& in,
+                                          const TileCopy<HP>& copy, int b, int tile)
 {
-    const int r0 = tile * kTile;
-    const uint32_t sk = smem_addr(sm.a[stage]), sv = smem_addr(sm.b[stage]);
-#pragma unroll
-    for (int i = 0; i < 2 * HP; ++i) {
-        const int id = i * kAttnThreads + (int)threadIdx.x;
-        const int c = id % (4 * HP), row = id / (4 * HP);
-        const int64_t key = (int64_t)b * in.Nk + r0 + row;
-        bool on = r0 + row < in.Nk;
-        if (on && in.kg != nullptr) on = __ldg(in.kg + key) >= 0;
-        const uint32_t dst = (c / 4) * kTileBytes + tile_at(row, c % 4);
-        cp_async<16>(sk + dst, on ? in.k + key * in.ldk + h * kDim + c * 8 : in.k, on);
-        cp_async<16>(sv + dst, on ? in.v + key * in.ldv + h * kDim + c * 8 : in.v, on);
-    }
-    if (threadIdx.x < kTile) {
-        const int row = r0 + threadIdx.x;
-        const int64_t key = (int64_t)b * in.Nk + row;
-        const bool on = row < in.Nk;
-        if constexpr (kBias)
-            cp_async<8>(smem_addr(&sm.pos[stage][threadIdx.x]), on ? in.kp + key : in.kp, on);
-        if (in.kg != nullptr)
-            cp_async<4>(smem_addr(&sm.group[stage][threadIdx.x]), on ? in.kg + key : in.kg, on);
-    }
+    const int64_t first = (int64_t)b * in.Nk;
+    const bool all = in.kg == nullptr && tile * kTile + kTile <= in.Nk;
+    copy.fetch(smem_addr(sm.a[stage]), smem_addr(sm.b[stage]), tile, all,
+               [&](int key) { return in.kg == nullptr || __ldg(in.kg + first + key) >= 0; });
+    load_columns<kBias>(sm.pos[stage], sm.group[stage], in.kp, in.kg, first, tile * kTile, in.Nk);
     cp_commit();
 }
 
@@ -75,73 +62,61 @@ __device__ __forceinline__ void load_keys(BackwardSmem<HP>& sm, int stage, const
 // their gradient hold, p = 0 then has nothing to meet.
 template <int HP, bool kBias>
 __device__ __forceinline__ void load_queries(BackwardSmem<HP>& sm, int stage,
-                                             const BackwardArgs& a, int b, int h, int tile)
+                                             const BackwardArgs& a, const TileCopy<HP>& copy,
+                                             int b, int h, int tile)
 {
     const Inputs& in = a.in;
     const int r0 = tile * kTile;
-    const uint32_t sq = smem_addr(sm.a[stage]), so = smem_addr(sm.b[stage]);
+    const float* lse = a.lse + ((int64_t)b * in.H + h + threadIdx.x % TileCopy<HP>::kChunks / 4) * in.Nq;
+    copy.fetch(smem_addr(sm.a[stage]), smem_addr(sm.b[stage]), tile, false,
+               [&](int q) { return __ldg(lse + q) != -INFINITY; });
+    const int64_t plane = (int64_t)in.B * in.H * in.Nq;
 #pragma unroll
-    for (int i = 0; i < 2 * HP; ++i) {
-        const int id = i * kAttnThreads + (int)threadIdx.x;
-        const int c = id % (4 * HP), row = id / (4 * HP);
-        const int64_t q = (int64_t)b * in.Nq + r0 + row;
-        bool on = r0 + row < in.Nq;
-        if (on)
-            on = __ldg(a.lse + ((int64_t)b * in.H + h + c / 4) * in.Nq + r0 + row) != -INFINITY;
-        const uint32_t dst = (c / 4) * kTileBytes + tile_at(row, c % 4);
-        cp_async<16>(sq + dst, on ? in.q + q * in.ldq + h * kDim + c * 8 : in.q, on);
-        cp_async<16>(so + dst, on ? a.go + (q * in.H + h) * kDim + c * 8 : a.go, on);
-    }
-    for (int i = threadIdx.x; i < HP * kTile; i += kAttnThreads) {
-        const int hh = i / kTile, row = r0 + i % kTile;
+    for (int i0 = 0; i0 < 3 * HP * kTile; i0 += kAttnThreads) {
+        const int i = i0 + (int)threadIdx.x;
+        if (3 * HP * kTile % kAttnThreads != 0 && i >= 3 * HP * kTile) break;
+        const int k = i / (HP * kTile), hh = i / kTile % HP, row = r0 + i % kTile;
         const bool on = row < in.Nq;
-        const float4* src = a.rows + ((int64_t)b * in.H + h + hh) * in.Nq + row;
-        cp_async<16>(smem_addr(&sm.rows[stage][hh][i % kTile]), on ? src : a.rows, on);
+        const float* src = a.rows + k * plane + ((int64_t)b * in.H + h + hh) * in.Nq + row;
+        cp_async<4>(smem_addr(&sm.rows[stage][hh][k][i % kTile]), on ? src : a.rows, on);
     }
-    if (threadIdx.x < kTile) {
-        const int row = r0 + threadIdx.x;
-        const int64_t q = (int64_t)b * in.Nq + row;
-        const bool on = row < in.Nq;
-        if constexpr (kBias)
-            cp_async<8>(smem_addr(&sm.pos[stage][threadIdx.x]), on ? in.qp + q : in.qp, on);
-        if (in.qg != nullptr)
-            cp_async<4>(smem_addr(&sm.group[stage][threadIdx.x]), on ? in.qg + q : in.qg, on);
-    }
+    load_columns<kBias>(sm.pos[stage], sm.group[stage], in.qp, in.qg, (int64_t)b * in.Nq, r0,
+                        in.Nq);
     cp_commit();
 }
 
-// A step's 16 x 32 products of a warp's rows with the tile's rows 32s..32s+31.
-__device__ __forceinline__ void products(float (&c)[4][4], const uint32_t (&f)[8], uint32_t tile,
-                                         int s, int lane)
+// A step's 16 x 32 products of a warp's rows with the tile's rows 32s..32s+31:
+// c[j][half] are the columns 8j + 2t, + 1 of the row g + 8 half.
+__device__ __forceinline__ void products(float2 (&c)[4][2], const uint32_t (&f)[8], uint32_t tile,
+                                         int s, const LaneAt& lanes)
 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         uint32_t r[4];
-        load_cols(r, tile, 4 * s + j, lane);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[j][i] = 0.0f;
-        mma(c[j], f, r[0], r[1]);
-        mma(c[j], f + 4, r[2], r[3]);
+        load_cols(r, tile, 4 * s + j, lanes);
+        float v[4];
+        mma_first(v, f, r[0], r[1]);
+        mma(v, f + 4, r[2], r[3]);
+        c[j][0] = pair(v, 0);
+        c[j][1] = pair(v, 1);
     }
 }
 
 // acc += w (16 x 32, rounded to bf16: the matrix instruction's type) times the
 // tile's rows 32s .. 32s + 31.
-__device__ __forceinline__ void accumulate(float (&acc)[4][4], const float (&w)[4][4],
-                                           uint32_t tile, int s, int lane)
+__device__ __forceinline__ void accumulate(float (&acc)[4][4], const float2 (&w)[4][2],
+                                           uint32_t tile, int s, const LaneAt& lanes)
 {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const uint32_t f[4] = {pack_bf16(w[2 * k][0], w[2 * k][1]),
-                               pack_bf16(w[2 * k][2], w[2 * k][3]),
-                               pack_bf16(w[2 * k + 1][0], w[2 * k + 1][1]),
-                               pack_bf16(w[2 * k + 1][2], w[2 * k + 1][3])};
+        const uint32_t f[4] = {pack_bf16(w[2 * k][0]), pack_bf16(w[2 * k][1]),
+                               pack_bf16(w[2 * k + 1][0]), pack_bf16(w[2 * k + 1][1])};
 #pragma unroll
-        for (int d = 0; d < 4; d += 2) {
+        for (int d = 0; d < 2; ++d) {
             uint32_t r[4];
-            load_sum(r, tile, 2 * s + k, d, lane);
-            mma(acc[d], f, r[0], r[1]);
-            mma(acc[d + 1], f, r[2], r[3]);
+            load_sum(r, tile, 2 * s + k, d, lanes);
+            mma(acc[2 * d], f, r[0], r[1]);
+            mma(acc[2 * d + 1], f, r[2], r[3]);
         }
     }
 }
@@ -159,18 +134,26 @@ __device__ __forceinline__ void store_rows(__nv_bfloat16* p, int64_t row, int64_
     }
 }
 
+// Replaces the values of a pair whose bits are set.
+__device__ __forceinline__ void mask(float2& v, uint32_t bits, float by)
+{
+    if (bits & 1) v.x = by;
+    if (bits & 2) v.y = by;
+}
+
 __device__ __forceinline__ float quad_sum(float x)
 {
     x += __shfl_xor_sync(0xffffffffu, x, 1);
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
-template <int HP, bool kBias>
-__global__ void __launch_bounds__(kAttnThreads) attention_grad_queries_kernel(const BackwardArgs a)
+// 64 queries and the tiles [begin, last) of the keys: D (and what the last
+// kernel needs of the queries beside it), or with kGrad, given D, dq and dtau.
+template <int HP, bool kBias, bool kGrad>
+__device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardArgs& a, int id,
+                                          int begin, int last, float* sums)
 {
-    __shared__ BackwardSmem<HP> sm;
     const Inputs& in = a.in;
-    int id = blockIdx.x;
     const int qt = id % a.q_tiles;
     id /= a.q_tiles;
     const int h = id % (in.H / HP) * HP, b = id / (in.H / HP);
@@ -180,175 +163,195 @@ __global__ void __launch_bounds__(kAttnThreads) attention_grad_queries_kernel(co
     const int64_t q0 = (int64_t)b * in.Nq + row;
 
     uint32_t qf[HP][8], of[HP][8];
-    float e0[HP], e1[HP], tau0[HP] = {}, tau1[HP] = {};
+    float e[HP][2], tau[HP][2] = {};  // -lse, -tau in units of log 2
+    float2 p[2] = {};
 #pragma unroll
     for (int hh = 0; hh < HP; ++hh) {
-        const int64_t i = ((int64_t)b * in.H + h + hh) * in.Nq + row;
-        e0[hh] = on0 ? __ldg(a.lse + i) : -INFINITY;
-        e1[hh] = on1 ? __ldg(a.lse + i + 8) : -INFINITY;
-        const bool live0 = e0[hh] != -INFINITY, live1 = e1[hh] != -INFINITY;
-        load_rows(qf[hh], in.q + (int64_t)b * in.Nq * in.ldq + (h + hh) * kDim, in.ldq, row, live0,
-                  live1, t);
+        bool live[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int64_t i = ((int64_t)b * in.H + h + hh) * in.Nq + row + 8 * half;
+            const float lse = (half ? on1 : on0) ? __ldg(a.lse + i) : -INFINITY;
+            live[half] = lse != -INFINITY;
+            // a row that sees nothing: weight exp2(s - infinity) = 0 everywhere
+            e[hh][half] = live[half] ? -lse * kLog2e : -INFINITY;
+            if constexpr (kBias) {
+                if (live[half])
+                    tau[hh][half] = -__ldg(in.tau + (q0 + 8 * half) * in.H + h + hh) * kLog2e;
+            }
+        }
+        load_rows(qf[hh], in.q + (int64_t)b * in.Nq * in.ldq + (h + hh) * kDim, in.ldq, row,
+                  live[0], live[1], t);
         load_rows(of[hh], a.go + ((int64_t)b * in.Nq * in.H + h + hh) * kDim,
-                  (int64_t)in.H * kDim, row, live0, live1, t);
-        // a row that sees nothing: weight exp2(s - infinity) = 0 everywhere
-        e0[hh] = live0 ? e0[hh] * kLog2e : INFINITY;
-        e1[hh] = live1 ? e1[hh] * kLog2e : INFINITY;
-        if constexpr (kBias) {
-            if (live0) tau0[hh] = __ldg(in.tau + q0 * in.H + h + hh) * kLog2e;
-            if (live1) tau1[hh] = __ldg(in.tau + (q0 + 8) * in.H + h + hh) * kLog2e;
+                  (int64_t)in.H * kDim, row, live[0], live[1], t);
+    }
+    if constexpr (kBias) {  // (a row that sees nothing may have any point)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (e[0][half] == -INFINITY) continue;
+            const float2 at = __ldg(in.qp + q0 + 8 * half);
+            p[half] = make_float2(-at.x, -at.y);
         }
     }
-    float2 p0{}, p1{};
-    if constexpr (kBias) {  // (a row that sees nothing may have any point)
-        if (e0[0] != INFINITY) p0 = __ldg(in.qp + q0);
-        if (e1[0] != INFINITY) p1 = __ldg(in.qp + q0 + 8);
-    }
     int g0 = 0, g1 = 0;
-    GroupRange own{0, 0, true, true, true};
+    GroupRange own{0, 0, true, true, true, true};
     if (in.qg != nullptr) {
         g0 = on0 ? __ldg(in.qg + q0) : -1;
         g1 = on1 ? __ldg(in.qg + q0 + 8) : -1;
         own = warp_range(in.qg, (int64_t)b * in.Nq + qt * kRows, min(kRows, in.Nq - qt * kRows));
     }
     const float scale = in.scale * kLog2e;
-    float D0[HP] = {}, D1[HP] = {}, dt0[HP] = {}, dt1[HP] = {}, dq[HP][4][4] = {};
+    float D[HP][2] = {}, dt[HP][2] = {}, dq[HP][4][4] = {};
+    const int64_t plane = (int64_t)in.B * in.H * in.Nq;
+    if constexpr (kGrad) {
+#pragma unroll
+        for (int hh = 0; hh < HP; ++hh)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                if (half ? on1 : on0)
+                    D[hh][half] = a.rows[2 * plane + ((int64_t)b * in.H + h + hh) * in.Nq + row +
+                                         8 * half];
+    }
 
-    const int tiles = a.k_tiles;
+    const LaneAt lanes = lane_at(lane);
+    const TileCopy<HP> copy(in.k + (int64_t)b * in.Nk * in.ldk + h * kDim, in.ldk,
+                            in.v + (int64_t)b * in.Nk * in.ldv + h * kDim, in.ldv, in.Nk);
+    for (int first = begin; first < last; first += kScan) {
+        __syncthreads();  // the bits of the tiles before are read
+        scan_tiles<false>(sm.bits, own, true, in.kg, (int64_t)b * in.Nk, in.Nk, first, last);
+        int tile = next_tile(sm.bits, first, first, last), stage = 0;
+        if (tile < last) load_keys<HP, kBias>(sm, stage, in, copy, b, tile);
+        while (tile < last) {
+            const int ahead = next_tile(sm.bits, tile + 1, first, last);
+            if (ahead < last) {
+                load_keys<HP, kBias>(sm, stage ^ 1, in, copy, b, ahead);
+                cp_wait<1>();
+            } else {
+                cp_wait<0>();
+            }
+            __syncthreads();
+            const bool clear =
+                (sm.bits.clear[(tile - first) >> 5] >> ((tile - first) & 31)) & 1;
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-        for (int first = 0; first < tiles; first += kScan) {
-            if (pass == 0 || tiles > kScan)
-                scan_tiles<false>(sm.bits, own, true, in.kg, (int64_t)b * in.Nk, in.Nk, first,
-                                  tiles);
-            int tile = next_tile(sm.bits, first, first, tiles), stage = 0;
-            if (tile < tiles) load_keys<HP, kBias>(sm, stage, in, b, h, tile);
-            while (tile < tiles) {
-                const int ahead = next_tile(sm.bits, tile + 1, first, tiles);
-                if (ahead < tiles) {
-                    load_keys<HP, kBias>(sm, stage ^ 1, in, b, h, ahead);
-                    cp_wait<1>();
-                } else {
-                    cp_wait<0>();
+            for (int st = 0; st < kTile / kHalf; ++st) {
+                float2 dist[4][2];
+                uint32_t hide = 0;
+                if constexpr (kBias) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int at = kHalf * st + 8 * j + 2 * t;
+                        const float2 x = *reinterpret_cast<const float2*>(&sm.pos[stage].x[at]);
+                        const float2 y = *reinterpret_cast<const float2*>(&sm.pos[stage].y[at]);
+                        dist[j][0] = distances(p[0].x, p[0].y, x, y);
+                        dist[j][1] = distances(p[1].x, p[1].y, x, y);
+                    }
                 }
-                __syncthreads();
-                const bool clear =
-                    (sm.bits.clear[(tile - first) >> 5] >> ((tile - first) & 31)) & 1;
+                if (!clear) {
 #pragma unroll
-                for (int st = 0; st < kTile / kHalf; ++st) {
-                    float dist[4][4];
-                    uint32_t hide = 0;
-                    if constexpr (kBias) {
+                    for (int j = 0; j < 4; ++j) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float4 pk = *reinterpret_cast<const float4*>(
-                                &sm.pos[stage][kHalf * st + 8 * j + 2 * t]);
-                            dist[j][0] = distance(p0, pk.x, pk.y);
-                            dist[j][1] = distance(p0, pk.z, pk.w);
-                            dist[j][2] = distance(p1, pk.x, pk.y);
-                            dist[j][3] = distance(p1, pk.z, pk.w);
+                        for (int c = 0; c < 2; ++c) {
+                            const int at = kHalf * st + 8 * j + 2 * t + c;
+                            const bool in_range = tile * kTile + at < in.Nk;
+                            const int kg = in.kg != nullptr ? sm.group[stage][at] : 0;
+                            hide |= (uint32_t)!(in_range && sees(g0, kg)) << (4 * j + c);
+                            hide |= (uint32_t)!(in_range && sees(g1, kg)) << (4 * j + 2 + c);
                         }
                     }
-                    if (!clear) {
+                    if constexpr (kBias) {  // a masked point may be anything
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
+                        for (int j = 0; j < 4; ++j)
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                const int at = kHalf * st + 8 * j + 2 * t + c;
-                                const bool in_range = tile * kTile + at < in.Nk;
-                                const int kg = in.kg != nullptr ? sm.group[stage][at] : 0;
-                                hide |= (uint32_t)!(in_range && sees(g0, kg)) << (4 * j + c);
-                                hide |= (uint32_t)!(in_range && sees(g1, kg)) << (4 * j + 2 + c);
-                            }
-                        }
-                        if constexpr (kBias) {  // a masked point may be anything
+                            for (int half = 0; half < 2; ++half)
+                                mask(dist[j][half], hide >> (4 * j + 2 * half), 0.0f);
+                    }
+                }
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
+                for (int hh = 0; hh < HP; ++hh) {
+                    const uint32_t sk = smem_addr(sm.a[stage]) + hh * kTileBytes;
+                    const uint32_t sv = smem_addr(sm.b[stage]) + hh * kTileBytes;
+                    float2 s[4][2], dp[4][2];
+                    products(s, qf[hh], sk, st, lanes);
+                    products(dp, of[hh], sv, st, lanes);
 #pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    if ((hide >> (4 * j + c)) & 1) dist[j][c] = 0.0f;
+                    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            float2 x = __ffma2_rn(s[j][half], both(scale), both(e[hh][half]));
+                            if constexpr (kBias)
+                                x = __ffma2_rn(dist[j][half], both(tau[hh][half]), x);
+                            if (!clear) mask(x, hide >> (4 * j + 2 * half), -INFINITY);
+                            s[j][half] = make_float2(exp2_approx(x.x), exp2_approx(x.y));
                         }
                     }
+                    float2 sum[2] = {both(0.0f), both(0.0f)};  // a step's own, then the total
+                    if constexpr (!kGrad) {
 #pragma unroll
-                    for (int hh = 0; hh < HP; ++hh) {
-                        const uint32_t sk = smem_addr(sm.a[stage]) + hh * kTileBytes;
-                        const uint32_t sv = smem_addr(sm.b[stage]) + hh * kTileBytes;
-                        float s[4][4], dp[4][4];
-                        products(s, qf[hh], sk, st, lane);
-                        products(dp, of[hh], sv, st, lane);
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int half = 0; half < 2; ++half)
+                                sum[half] = __ffma2_rn(s[j][half], dp[j][half], sum[half]);
+                        D[hh][0] += sum[0].x + sum[0].y;
+                        D[hh][1] += sum[1].x + sum[1].y;
+                    } else {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                float x = fmaf(s[j][c], scale, c < 2 ? -e0[hh] : -e1[hh]);
+                            for (int half = 0; half < 2; ++half) {
+                                s[j][half] = __fmul2_rn(
+                                    s[j][half], __fadd2_rn(dp[j][half], both(-D[hh][half])));
                                 if constexpr (kBias)
-                                    x = fmaf(c < 2 ? -tau0[hh] : -tau1[hh], dist[j][c], x);
-                                if ((hide >> (4 * j + c)) & 1) x = -INFINITY;
-                                s[j][c] = exp2_approx(x);
+                                    sum[half] =
+                                        __ffma2_rn(s[j][half], dist[j][half], sum[half]);
                             }
                         }
-                        if (pass == 0) {
-                            float a0 = 0.0f, a1 = 0.0f;  // a step's own sums, then the total
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                a0 = fmaf(s[j][0], dp[j][0], fmaf(s[j][1], dp[j][1], a0));
-                                a1 = fmaf(s[j][2], dp[j][2], fmaf(s[j][3], dp[j][3], a1));
-                            }
-                            D0[hh] += a0;
-                            D1[hh] += a1;
-                        } else {
-                            float a0 = 0.0f, a1 = 0.0f;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                                for (int c = 0; c < 4; ++c) {
-                                    s[j][c] *= dp[j][c] - (c < 2 ? D0[hh] : D1[hh]);
-                                    if constexpr (kBias) {
-                                        if (c < 2) a0 = fmaf(s[j][c], dist[j][c], a0);
-                                        else a1 = fmaf(s[j][c], dist[j][c], a1);
-                                    }
-                                }
-                            }
-                            dt0[hh] += a0;
-                            dt1[hh] += a1;
-                            accumulate(dq[hh], s, sk, st, lane);
-                        }
+                        dt[hh][0] += sum[0].x + sum[0].y;
+                        dt[hh][1] += sum[1].x + sum[1].y;
+                        accumulate(dq[hh], s, sk, st, lanes);
                     }
                 }
-                __syncthreads();
-                tile = ahead;
-                stage ^= 1;
             }
-        }
-        if (pass == 0) {
-#pragma unroll
-            for (int hh = 0; hh < HP; ++hh) {
-                D0[hh] = quad_sum(D0[hh]);
-                D1[hh] = quad_sum(D1[hh]);
-                const int64_t i = ((int64_t)b * in.H + h + hh) * in.Nq + row;
-                if (t == 0 && on0) a.rows[i] = make_float4(e0[hh], tau0[hh], D0[hh], 0.0f);
-                if (t == 0 && on1) a.rows[i + 8] = make_float4(e1[hh], tau1[hh], D1[hh], 0.0f);
-            }
+            __syncthreads();
+            tile = ahead;
+            stage ^= 1;
         }
     }
+    if constexpr (!kGrad) {
 #pragma unroll
-    for (int hh = 0; hh < HP; ++hh) {
-        store_rows(a.dq, q0, in.H, h + hh, dq[hh], in.scale, on0, on1, t);
-        if constexpr (kBias) {
-            dt0[hh] = quad_sum(dt0[hh]);
-            dt1[hh] = quad_sum(dt1[hh]);
-            if (t == 0 && on0) a.dtau[q0 * in.H + h + hh] = -dt0[hh];
-            if (t == 0 && on1) a.dtau[(q0 + 8) * in.H + h + hh] = -dt1[hh];
+        for (int hh = 0; hh < HP; ++hh) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                D[hh][half] = quad_sum(D[hh][half]);
+                if (t != 0 || !(half ? on1 : on0)) continue;
+                const int64_t i = ((int64_t)b * in.H + h + hh) * in.Nq + row + 8 * half;
+                sums[i] = D[hh][half];
+                if (begin == 0) {
+                    a.rows[i] = e[hh][half];
+                    a.rows[plane + i] = tau[hh][half];
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int hh = 0; hh < HP; ++hh) {
+            store_rows(a.dq, q0, in.H, h + hh, dq[hh], in.scale, on0, on1, t);
+            if constexpr (kBias) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float sum = quad_sum(dt[hh][half]);
+                    if (t == 0 && (half ? on1 : on0))
+                        a.dtau[(q0 + 8 * half) * in.H + h + hh] = -sum;
+                }
+            }
         }
     }
 }
 
+// 64 keys and all queries: dk and dv.
 template <int HP, bool kBias>
-__global__ void __launch_bounds__(kAttnThreads) attention_grad_keys_kernel(const BackwardArgs a)
+__device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const BackwardArgs& a, int id)
 {
-    __shared__ BackwardSmem<HP> sm;
     const Inputs& in = a.in;
-    int id = blockIdx.x;
     const int kt = id % a.k_tiles;
     id /= a.k_tiles;
     const int h = id % (in.H / HP) * HP, b = id / (in.H / HP);
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(kAttnThreads) attention_grad_keys_kernel(const
     const bool on0 = row < in.Nk, on1 = row + 8 < in.Nk;
     const int64_t k0 = (int64_t)b * in.Nk + row;
     int g0 = on0 ? 0 : -1, g1 = on1 ? 0 : -1;
-    GroupRange own{0, 0, true, true, true};
+    GroupRange own{0, 0, true, true, true, true};
     const int own_rows = min(kRows, in.Nk - kt * kRows);
     if (in.kg != nullptr) {
         if (on0) g0 = __ldg(in.kg + k0);
@@ -372,43 +375,51 @@ __global__ void __launch_bounds__(kAttnThreads) attention_grad_keys_kernel(const
         load_rows(vf[hh], in.v + (int64_t)b * in.Nk * in.ldv + (h + hh) * kDim, in.ldv, row,
                   g0 >= 0, g1 >= 0, t);
     }
-    float2 p0{}, p1{};
+    float2 p[2] = {};
     if constexpr (kBias) {
-        if (g0 >= 0) p0 = __ldg(in.kp + k0);
-        if (g1 >= 0) p1 = __ldg(in.kp + k0 + 8);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if ((half ? g1 : g0) < 0) continue;
+            const float2 at = __ldg(in.kp + k0 + 8 * half);
+            p[half] = make_float2(-at.x, -at.y);
+        }
     }
     const float scale = in.scale * kLog2e;
     float dk[HP][4][4] = {}, dv[HP][4][4] = {};
 
+    const LaneAt lanes = lane_at(lane);
+    const TileCopy<HP> copy(in.q + (int64_t)b * in.Nq * in.ldq + h * kDim, in.ldq,
+                            a.go + ((int64_t)b * in.Nq * in.H + h) * kDim, (int64_t)in.H * kDim,
+                            in.Nq);
     const int tiles = a.q_tiles;
     for (int first = 0; first < tiles; first += kScan) {
+        __syncthreads();
         scan_tiles<true>(sm.bits, own, own_rows == kRows, in.qg, (int64_t)b * in.Nq, in.Nq, first,
                          tiles);
         int tile = next_tile(sm.bits, first, first, tiles), stage = 0;
-        if (tile < tiles) load_queries<HP, kBias>(sm, stage, a, b, h, tile);
+        if (tile < tiles) load_queries<HP, kBias>(sm, stage, a, copy, b, h, tile);
         while (tile < tiles) {
             const int ahead = next_tile(sm.bits, tile + 1, first, tiles);
             if (ahead < tiles) {
-                load_queries<HP, kBias>(sm, stage ^ 1, a, b, h, ahead);
+                load_queries<HP, kBias>(sm, stage ^ 1, a, copy, b, h, ahead);
                 cp_wait<1>();
             } else {
                 cp_wait<0>();
             }
             __syncthreads();
             const bool clear = (sm.bits.clear[(tile - first) >> 5] >> ((tile - first) & 31)) & 1;
-#pragma unroll
+#pragma unroll 1
             for (int st = 0; st < kTile / kHalf; ++st) {
-                float dist[4][4];
+                float2 dist[4][2];
                 uint32_t hide = 0;
                 if constexpr (kBias) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float4 pq = *reinterpret_cast<const float4*>(
-                            &sm.pos[stage][kHalf * st + 8 * j + 2 * t]);
-                        dist[j][0] = distance(p0, pq.x, pq.y);
-                        dist[j][1] = distance(p0, pq.z, pq.w);
-                        dist[j][2] = distance(p1, pq.x, pq.y);
-                        dist[j][3] = distance(p1, pq.z, pq.w);
+                        const int at = kHalf * st + 8 * j + 2 * t;
+                        const float2 x = *reinterpret_cast<const float2*>(&sm.pos[stage].x[at]);
+                        const float2 y = *reinterpret_cast<const float2*>(&sm.pos[stage].y[at]);
+                        dist[j][0] = distances(p[0].x, p[0].y, x, y);
+                        dist[j][1] = distances(p[1].x, p[1].y, x, y);
                     }
                 }
                 if (!clear) {
@@ -428,27 +439,29 @@ __global__ void __launch_bounds__(kAttnThreads) attention_grad_keys_kernel(const
                 for (int hh = 0; hh < HP; ++hh) {
                     const uint32_t sq = smem_addr(sm.a[stage]) + hh * kTileBytes;
                     const uint32_t so = smem_addr(sm.b[stage]) + hh * kTileBytes;
-                    float s[4][4], dp[4][4];
-                    products(s, kf[hh], sq, st, lane);
-                    products(dp, vf[hh], so, st, lane);
+                    float2 s[4][2], dp[4][2];
+                    products(s, kf[hh], sq, st, lanes);
+                    products(dp, vf[hh], so, st, lanes);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
+                        const int at = kHalf * st + 8 * j + 2 * t;
+                        float2 r[3];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const float4 r = sm.rows[stage][hh][kHalf * st + 8 * j + 2 * t + c];
+                        for (int k = 0; k < 3; ++k)
+                            r[k] = *reinterpret_cast<const float2*>(&sm.rows[stage][hh][k][at]);
 #pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                const int i = 2 * half + c;
-                                float x = fmaf(s[j][i], scale, -r.x);
-                                if constexpr (kBias) x = fmaf(-r.y, dist[j][i], x);
-                                if ((hide >> (4 * j + i)) & 1) x = -INFINITY;
-                                s[j][i] = exp2_approx(x);
-                                dp[j][i] = s[j][i] * (dp[j][i] - r.z);
-                            }
+                        for (int half = 0; half < 2; ++half) {
+                            float2 x = __ffma2_rn(s[j][half], both(scale), r[0]);
+                            if constexpr (kBias) x = __ffma2_rn(dist[j][half], r[1], x);
+                            if (!clear) mask(x, hide >> (4 * j + 2 * half), -INFINITY);
+                            s[j][half] = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                            dp[j][half] = __fmul2_rn(
+                                s[j][half],
+                                __fadd2_rn(dp[j][half], make_float2(-r[2].x, -r[2].y)));
                         }
                     }
-                    accumulate(dv[hh], s, so, st, lane);
-                    accumulate(dk[hh], dp, sq, st, lane);
+                    accumulate(dv[hh], s, so, st, lanes);
+                    accumulate(dk[hh], dp, sq, st, lanes);
                 }
             }
             __syncthreads();
@@ -464,18 +477,86 @@ __global__ void __launch_bounds__(kAttnThreads) attention_grad_keys_kernel(const
 }
 
 template <int HP, bool kBias>
-cudaError_t run(const BackwardArgs& a, cudaStream_t s)
+__global__ void __launch_bounds__(kAttnThreads, kBlocks) attention_dots_kernel(const BackwardArgs a)
 {
-    const int64_t per = (int64_t)a.in.B * (a.in.H / HP);
+    __shared__ BackwardSmem<HP> sm;
+    const int64_t plane = (int64_t)a.in.B * a.in.H * a.in.Nq;
+    const int per = a.q_tiles * (a.in.H / HP) * a.in.B;
+    const int split = blockIdx.x / per, begin = split * a.split_tiles;
+    walk_keys<HP, kBias, false>(sm, a, blockIdx.x - split * per, begin,
+                                min(a.k_tiles, begin + a.split_tiles),
+                                a.splits == 1 ? a.rows + 2 * plane : a.part + split * plane);
+}
+
+__global__ void __launch_bounds__(256) attention_dots_join_kernel(const BackwardArgs a)
+{
+    const int64_t plane = (int64_t)a.in.B * a.in.H * a.in.Nq;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    pdl_wait();
+    if (i >= plane) return;
+    float sum = 0.0f;
+    for (int s = 0; s < a.splits; ++s) sum += a.part[s * plane + i];
+    a.rows[2 * plane + i] = sum;
+}
+
+template <bool kBias>
+__global__ void __launch_bounds__(kAttnThreads, kBlocks) attention_grad_kernel(const BackwardArgs a)
+{
+    __shared__ BackwardSmem<1> sm;
+    const int keys = a.k_tiles * a.in.H * a.in.B;  // the longer ones first
+    if ((int)blockIdx.x < keys) walk_queries<1, kBias>(sm, a, blockIdx.x);
+    else walk_keys<1, kBias, true>(sm, a, blockIdx.x - keys, 0, a.k_tiles, nullptr);
+}
+
+// CTAs of the first kernel: as in the forward, the keys are split until they
+// fill a wave, and where halves or thirds even out the last one.
+struct Plan {
+    int heads, splits, split_tiles;
+};
+
+Plan plan_of(int B, int Nq, int Nk, int H, bool bias)
+{
+    Plan p;
+    const int64_t wave = kBlocks * kSms;
+    const int tiles = (Nk + kTile - 1) / kTile;
+    int64_t ctas = (int64_t)((Nq + kTile - 1) / kTile) * B * H;
+    p.heads = bias && H % 2 == 0 && ctas >= 2 * wave ? 2 : 1;
+    ctas /= p.heads;
+    int64_t splits = wave / std::max<int64_t>(ctas, 1);
+    if (splits <= 1) {
+        double least = 1e30;
+        for (int s = 1; s <= 4; ++s) {
+            const double cost = (double)((ctas * s + wave - 1) / wave) / s + 0.02 * (s - 1);
+            if (cost < least) {
+                least = cost;
+                splits = s;
+            }
+        }
+    }
+    splits = std::max<int64_t>(1, std::min<int64_t>({splits, (tiles + 1) / 2, kMaxSplits}));
+    p.split_tiles = std::max<int>(1, (tiles + (int)splits - 1) / (int)splits);
+    p.splits = std::max(1, (tiles + p.split_tiles - 1) / p.split_tiles);
+    return p;
+}
+
+cudaError_t run(const BackwardArgs& a, const Plan& plan, bool bias, cudaStream_t s)
+{
+    const int64_t items = (int64_t)a.in.B * a.in.H;
+    cudaError_t e = cudaSuccess;
     if (a.in.Nq > 0) {
-        attention_grad_queries_kernel<HP, kBias>
-            <<<(unsigned)(per * a.q_tiles), kAttnThreads, 0, s>>>(a);
-        const cudaError_t e = cudaGetLastError();
+        const unsigned ctas = (unsigned)(items / plan.heads * a.q_tiles * a.splits);
+        if (plan.heads == 2) attention_dots_kernel<2, true><<<ctas, kAttnThreads, 0, s>>>(a);
+        else if (bias) attention_dots_kernel<1, true><<<ctas, kAttnThreads, 0, s>>>(a);
+        else attention_dots_kernel<1, false><<<ctas, kAttnThreads, 0, s>>>(a);
+        e = cudaGetLastError();
+        if (e == cudaSuccess && a.splits > 1)
+            e = launch_pdl(attention_dots_join_kernel,
+                           dim3((unsigned)((items * a.in.Nq + 255) / 256)), dim3(256), 0, s, a);
         if (e != cudaSuccess) return e;
     }
-    if (a.in.Nk > 0)
-        attention_grad_keys_kernel<HP, kBias>
-            <<<(unsigned)(per * a.k_tiles), kAttnThreads, 0, s>>>(a);
+    const unsigned ctas = (unsigned)(items * (a.q_tiles + a.k_tiles));
+    if (bias) attention_grad_kernel<true><<<ctas, kAttnThreads, 0, s>>>(a);
+    else attention_grad_kernel<false><<<ctas, kAttnThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -489,7 +570,8 @@ using namespace msda::attn;
 extern "C" size_t msda_query_attention_backward_workspace_size(const msda_attention_t* p)
 {
     if (p == nullptr || p->B <= 0 || p->Nq <= 0 || p->H < 1) return 0;
-    return sizeof(float4) * (size_t)p->B * p->H * p->Nq;
+    const Plan plan = plan_of(p->B, p->Nq, p->Nk, p->H, p->tau != nullptr);
+    return (size_t)(3 + (plan.splits > 1 ? plan.splits : 0)) * sizeof(float) * p->B * p->H * p->Nq;
 }
 
 extern "C" msda_status_t msda_query_attention_backward(const msda_attention_t* p, const float* lse,
@@ -531,10 +613,14 @@ extern "C" msda_status_t msda_query_attention_backward(const msda_attention_t* p
     a.dk = static_cast<__nv_bfloat16*>(grad_k);
     a.dv = static_cast<__nv_bfloat16*>(grad_v);
     a.dtau = grad_tau;
-    a.rows = static_cast<float4*>(workspace);
+    const Plan plan = plan_of(p->B, p->Nq, p->Nk, p->H, p->tau != nullptr);
+    a.rows = static_cast<float*>(workspace);
+    a.part = a.rows + 3 * rows_q;
+    a.splits = plan.splits;
+    a.split_tiles = plan.split_tiles;
     a.q_tiles = (p->Nq + kTile - 1) / kTile;
     a.k_tiles = (p->Nk + kTile - 1) / kTile;
     const cudaStream_t s = (cudaStream_t)stream;
-    const cudaError_t e = p->tau != nullptr ? run<1, true>(a, s) : run<1, false>(a, s);
+    const cudaError_t e = run(a, plan, p->tau != nullptr, s);
     return api_cuda(e, "msda_query_attention_backward");
 }
