@@ -21,6 +21,7 @@ and ``msda_backward`` (``deterministic=True``: the fixed-point variants),
 entry points (workspace sizes, status strings, the no-alloc compaction, the
 GEMM's timeout counter and test switch) are reached through ``lib()``.
 """
+import array
 import contextlib
 import ctypes
 import operator
@@ -248,11 +249,10 @@ def _contig(*ts):
 _HERE_ALREADY = contextlib.nullcontext()
 
 
-def _scope(name, stream, first, *others):
+def _scope(torch, name, stream, first, *others):
     """The context of a call on the tensors' device: that device current and
     `stream` (of that device), when given, the current stream, so that what is
     allocated inside belongs to the stream that the kernels run on."""
-    torch = _torch()
     index = first.get_device()
     for t in others:
         if t is not None and t.get_device() != index:
@@ -267,9 +267,9 @@ def _scope(name, stream, first, *others):
     return _HERE_ALREADY if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
-def _raw_stream(tensor):
+def _raw_stream(torch, tensor):
     """The handle of the tensor's device's current stream (as an integer)."""
-    return _torch()._C._cuda_getCurrentRawStream(tensor.get_device())
+    return torch._C._cuda_getCurrentRawStream(tensor.get_device())
 
 
 def _address(t):
@@ -766,10 +766,6 @@ def sca_backward_inputs(spatial_shapes, level_start_index, attention_logits, pos
     return g_off, g_lg, g_ref
 
 
-_GRAD_T = np.dtype([("grad", np.uintp), ("out", np.uintp), ("numel", np.int64),
-                    ("grad_dtype", np.int32), ("out_dtype", np.int32)])
-
-
 def _same_dense_layout(a, b):
     """Whether a and b hold one value per element in the same order, without gaps."""
     torch = _torch()
@@ -796,38 +792,42 @@ def msda_clip_grad_norm(grads, max_norm, eps=1e-6, grad_scale=1.0, out=None, tot
     # one pass over the list per attribute, each a C-level map: of a list of
     # hundreds these lines are most of the call's host time
     every = grads if out is None else grads + outs
-    Tensor = torch.Tensor
+    Tensor, dtype_of = torch.Tensor, operator.attrgetter("dtype")
     first = every[0] if n else total_norm
     if first.get_device() < 0 or len(set(map(Tensor.get_device, every))) > 1:
         raise MsdaError("msda_clip_grad_norm: the tensors must be on one CUDA device")
-    dtypes = list(map(operator.attrgetter("dtype"), every))
     codes = {torch.float32: MSDA_F32, torch.bfloat16: MSDA_BF16}
-    if not codes.keys() >= set(dtypes):
+    kinds = [set(map(dtype_of, grads)), set(map(dtype_of, outs))]
+    if not codes.keys() >= kinds[0] | kinds[1]:
         raise MsdaError("msda_clip_grad_norm: a tensor is neither float32 nor bfloat16")
-    sizes = list(map(Tensor.numel, every))
+    sizes = list(map(Tensor.numel, grads))
     if not all(map(Tensor.is_contiguous, every)):
         if not all(g.shape == o.shape and _same_dense_layout(g, o) for g, o in zip(grads, outs)):
             raise MsdaError("msda_clip_grad_norm: a tensor is not dense, or an output is not "
                             "laid out as its gradient")
-    elif out is not None and sizes[:n] != sizes[n:]:
+    elif out is not None and sizes != list(map(Tensor.numel, outs)):
         raise MsdaError("msda_clip_grad_norm: an output has another size than its gradient")
-    pointers = list(map(Tensor.data_ptr, every))
-    kinds = list(map(codes.get, dtypes))
-    table = np.empty(n, _GRAD_T)
-    table["grad"], table["out"] = pointers[:n], pointers[-n:] if n else []
-    table["numel"] = sizes[:n]
-    table["grad_dtype"], table["out_dtype"] = kinds[:n], kinds[-n:] if n else []
-    with _scope("msda_clip_grad_norm", stream, first, total_norm, workspace):
+    # msda_grad_t as four 64-bit words, the two dtypes in the last
+    words = [0] * (4 * n)
+    words[0::4] = map(Tensor.data_ptr, grads)
+    words[1::4] = words[0::4] if out is None else map(Tensor.data_ptr, outs)
+    words[2::4] = sizes
+    if len(kinds[0]) < 2 and len(kinds[1]) < 2:
+        words[3::4] = [codes[dtype_of(grads[0])] | codes[dtype_of(outs[0])] << 32] * n if n else []
+    else:
+        words[3::4] = [codes[g.dtype] | codes[o.dtype] << 32 for g, o in zip(grads, outs)]
+    table = array.array("Q", words)
+    with _scope(torch, "msda_clip_grad_norm", stream, first, total_norm, workspace):
         if total_norm is None:
             total_norm = torch.empty(1, device=first.device, dtype=torch.float32)
         elif total_norm.dtype != torch.float32 or total_norm.numel() != 1:
             raise MsdaError("msda_clip_grad_norm: total_norm must be one float32 value")
         workspace = _workspace(int(lib().msda_clip_grad_norm_workspace_size(n)), first.device,
                                workspace)
-        _check(lib().msda_clip_grad_norm(table.ctypes.data, n, max_norm, eps,
+        _check(lib().msda_clip_grad_norm(table.buffer_info()[0], n, max_norm, eps,
                                          grad_scale, _address(workspace),
                                          workspace.numel() * workspace.element_size(),
-                                         _address(total_norm), _raw_stream(first)),
+                                         _address(total_norm), _raw_stream(torch, first)),
                "msda_clip_grad_norm")
     return total_norm
 
@@ -847,10 +847,10 @@ def _arg(name, t, shape, dtypes, what):
         raise MsdaError(f"{name}: {what} must be contiguous")
 
 
-def _out(name, t, shape, dtypes, what, device):
-    """An output: the given tensor, checked, or a new one of dtypes[0]."""
+def _out(name, t, shape, dtypes, what, like):
+    """An output: the given tensor, checked, or a new one of dtypes[0] beside `like`."""
     if t is None:
-        return _torch().empty(shape, device=device, dtype=dtypes[0])
+        return like.new_empty(shape, dtype=dtypes[0])
     _arg(name, t, shape, dtypes, what)
     return t
 
@@ -888,19 +888,19 @@ def msda_group_norm(x, spatial_shapes, level_start_index, num_groups, gamma=None
                                    beta, activation)
     f32, data = (torch.float32,), (torch.float32, torch.bfloat16)
     small = tuple(x.shape[:-2]) + (d.L, d.G)
-    with _scope(name, stream, x, gamma, beta, out, mean, rstd, workspace):
+    with _scope(torch, name, stream, x, gamma, beta, out, mean, rstd, workspace):
         y = _out(name, out, x.shape, data if out is not None else (out_dtype or x.dtype,), "out",
-                 x.device)
+                 x)
         if out_dtype is not None and y.dtype != out_dtype:
             raise MsdaError(f"{name}: out is {y.dtype}, not {out_dtype}")
-        mean = _out(name, mean, small, f32, "mean", x.device)
-        rstd = _out(name, rstd, small, f32, "rstd", x.device)
+        mean = _out(name, mean, small, f32, "mean", x)
+        rstd = _out(name, rstd, small, f32, "rstd", x)
         workspace = _workspace(int(lib().msda_group_norm_workspace_size(d)), x.device, workspace)
         _check(lib().msda_group_norm(_address(x), _vdt(x), shapes.ctypes.data,
                                      starts.ctypes.data, d, _address(gamma), _address(beta),
                                      eps, _ACTIVATIONS[activation], _vdt(y), _address(y), _address(mean),
                                      _address(rstd), _address(workspace), workspace.numel(),
-                                     _raw_stream(x)), name)
+                                     _raw_stream(torch, x)), name)
     return y, mean, rstd
 
 
@@ -920,20 +920,20 @@ def msda_group_norm_backward(x, spatial_shapes, level_start_index, num_groups, m
     _arg(name, rstd, small, f32, "rstd")
     _arg(name, grad_out, x.shape, data, "grad_out")
     gx, gg, gb = out if out is not None else (None, None, None)
-    with _scope(name, stream, x, gamma, beta, mean, rstd, grad_out, gx, gg, gb, workspace):
+    with _scope(torch, name, stream, x, gamma, beta, mean, rstd, grad_out, gx, gg, gb, workspace):
         gx = _out(name, gx, x.shape, data if gx is not None else (out_dtype or x.dtype,), "grad_x",
-                  x.device)
+                  x)
         if out_dtype is not None and gx.dtype != out_dtype:
             raise MsdaError(f"{name}: grad_x is {gx.dtype}, not {out_dtype}")
-        gg = _out(name, gg, (d.L, d.C), f32, "grad_gamma", x.device)
-        gb = _out(name, gb, (d.L, d.C), f32, "grad_beta", x.device)
+        gg = _out(name, gg, (d.L, d.C), f32, "grad_gamma", x)
+        gb = _out(name, gb, (d.L, d.C), f32, "grad_beta", x)
         workspace = _workspace(int(lib().msda_group_norm_backward_workspace_size(d)), x.device,
                                workspace)
         _check(lib().msda_group_norm_backward(
             _address(x), _vdt(x), shapes.ctypes.data, starts.ctypes.data, d,
             _address(gamma), _address(beta), _address(mean), _address(rstd), _ACTIVATIONS[activation],
             _address(grad_out), _vdt(grad_out), _vdt(gx), _address(gx), _address(gg), _address(gb),
-            _address(workspace), workspace.numel(), _raw_stream(x)), name)
+            _address(workspace), workspace.numel(), _raw_stream(torch, x)), name)
     return gx, gg, gb
 
 
@@ -986,16 +986,16 @@ def msda_query_attention(q, k, v, q_points=None, k_points=None, tau=None, q_grou
     torch = _torch()
     name = "msda_query_attention"
     p = _attention_args(name, q, k, v, q_points, k_points, tau, q_group, k_group, scale)
-    with _scope(name, stream, q, k, v, q_points, k_points, tau, q_group, k_group, out, lse,
+    with _scope(torch, name, stream, q, k, v, q_points, k_points, tau, q_group, k_group, out, lse,
                 workspace):
-        out = _out(name, out, (p.B, p.Nq, p.H * HEAD_DIM), (torch.bfloat16,), "out", q.device)
-        lse = _out(name, lse, (p.B, p.H, p.Nq), (torch.float32,), "lse", q.device)
+        out = _out(name, out, (p.B, p.Nq, p.H * HEAD_DIM), (torch.bfloat16,), "out", q)
+        lse = _out(name, lse, (p.B, p.H, p.Nq), (torch.float32,), "lse", q)
         need = int(lib().msda_query_attention_workspace_size(p))
         if need:
             workspace = _workspace(need, q.device, workspace)
         _check(lib().msda_query_attention(p, _address(out), _address(lse), _address(workspace),
                                           workspace.numel() if workspace is not None else 0,
-                                          _raw_stream(q)), name)
+                                          _raw_stream(torch, q)), name)
     return out, lse
 
 
@@ -1013,15 +1013,15 @@ def msda_query_attention_backward(q, k, v, lse, grad_out, q_points=None, k_point
     _arg(name, lse, (p.B, p.H, p.Nq), f32, "lse")
     _arg(name, grad_out, (p.B, p.Nq, p.H * HEAD_DIM), b16, "grad_out")
     gq, gk, gv, gt = out if out is not None else (None,) * 4
-    with _scope(name, stream, q, k, v, q_points, k_points, tau, q_group, k_group, lse, grad_out,
+    with _scope(torch, name, stream, q, k, v, q_points, k_points, tau, q_group, k_group, lse, grad_out,
                 gq, gk, gv, gt, workspace):
-        gq = _out(name, gq, q.shape, b16, "grad_q", q.device)
-        gk = _out(name, gk, k.shape, b16, "grad_k", q.device)
-        gv = _out(name, gv, v.shape, b16, "grad_v", q.device)
-        gt = _out(name, gt, tau.shape, f32, "grad_tau", q.device) if tau is not None else None
+        gq = _out(name, gq, q.shape, b16, "grad_q", q)
+        gk = _out(name, gk, k.shape, b16, "grad_k", q)
+        gv = _out(name, gv, v.shape, b16, "grad_v", q)
+        gt = _out(name, gt, tau.shape, f32, "grad_tau", q) if tau is not None else None
         need = int(lib().msda_query_attention_backward_workspace_size(p))
         workspace = _workspace(need, q.device, workspace)
         _check(lib().msda_query_attention_backward(
             p, _address(lse), _address(grad_out), _address(gq), _address(gk), _address(gv), _address(gt),
-            _address(workspace), workspace.numel(), _raw_stream(q)), name)
+            _address(workspace), workspace.numel(), _raw_stream(torch, q)), name)
     return gq, gk, gv, gt

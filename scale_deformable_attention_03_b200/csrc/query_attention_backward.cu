@@ -232,7 +232,7 @@ __device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardAr
             __syncthreads();
             const bool clear =
                 (sm.bits.clear[(tile - first) >> 5] >> ((tile - first) & 31)) & 1;
-#pragma unroll 1
+#pragma unroll
             for (int st = 0; st < kTile / kHalf; ++st) {
                 float2 dist[4][2];
                 uint32_t hide = 0;
@@ -408,7 +408,7 @@ __device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const Backwar
             }
             __syncthreads();
             const bool clear = (sm.bits.clear[(tile - first) >> 5] >> ((tile - first) & 31)) & 1;
-#pragma unroll 1
+#pragma unroll
             for (int st = 0; st < kTile / kHalf; ++st) {
                 float2 dist[4][2];
                 uint32_t hide = 0;
