@@ -119,6 +119,11 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool on)
                      : "memory");
 }
 
+__device__ __forceinline__ void cp_async_all(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 template <int kLeft>
@@ -204,13 +209,23 @@ struct TileCopy {
         const char *pa = a + r0 * lda, *pb = b + r0 * ldb;
         // (the places of a chunk repeat every eight rows, and kStep is a multiple of that)
         static_assert(kStep % 8 == 0, "");
+        const uint32_t ta = sa + to, tb = sb + to;
+        if (all) {
 #pragma unroll
+            for (int i = 0; i < kTile / kStep; ++i) {
+                cp_async_all(ta + i * kStep * 64, pa);
+                cp_async_all(tb + i * kStep * 64, pb);
+                pa += kStep * lda;
+                pb += kStep * ldb;
+            }
+            return;
+        }
+#pragma unroll 1
         for (int i = 0; i < kTile / kStep; ++i) {
-            const uint32_t at = to + i * kStep * 64;
-            bool there = true;
-            if (!all) there = tile * kTile + row + i * kStep < n && on(tile * kTile + row + i * kStep);
-            cp_async<16>(sa + at, there ? pa : a - row * lda, there);
-            cp_async<16>(sb + at, there ? pb : b - row * ldb, there);
+            const int r = tile * kTile + row + i * kStep;
+            const bool there = r < n && on(r);
+            cp_async<16>(ta + i * kStep * 64, there ? pa : a - row * lda, there);
+            cp_async<16>(tb + i * kStep * 64, there ? pb : b - row * ldb, there);
             pa += kStep * lda;
             pb += kStep * ldb;
         }
@@ -314,6 +329,27 @@ __device__ __forceinline__ int next_tile(const TileBits& bits, int tile, int fir
     }
     return last;
 }
+
+// The tiles from `first` on, up to `last`: all of them without groups, those
+// that have been looked up with.
+struct Tiles {
+    const TileBits& bits;
+    bool grouped;
+    int first, last;
+    int full;  // without groups: tiles below it have no pair masked
+
+    __device__ __forceinline__ int next(int tile) const
+    {
+        return grouped ? next_tile(bits, tile, first, last) : min(tile, last);
+    }
+    __device__ __forceinline__ bool clear(int tile) const
+    {
+        const int i = tile - first;
+        return grouped ? (bits.clear[i >> 5] >> (i & 31)) & 1 : tile < full;
+    }
+    // Where the tiles after these start.
+    __device__ __forceinline__ int end() const { return grouped ? first + kScan : last; }
+};
 
 __device__ __forceinline__ bool sees(int q_group, int k_group)
 {

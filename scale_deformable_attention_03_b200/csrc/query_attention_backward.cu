@@ -216,13 +216,18 @@ __device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardAr
     const LaneAt lanes = lane_at(lane);
     const TileCopy<HP> copy(in.k + (int64_t)b * in.Nk * in.ldk + h * kDim, in.ldk,
                             in.v + (int64_t)b * in.Nk * in.ldv + h * kDim, in.ldv, in.Nk);
-    for (int first = begin; first < last; first += kScan) {
-        __syncthreads();  // the bits of the tiles before are read
-        scan_tiles<false>(sm.bits, own, true, in.kg, (int64_t)b * in.Nk, in.Nk, first, last);
-        int tile = next_tile(sm.bits, first, first, last), stage = 0;
+    for (int first = begin; first < last;) {
+        const Tiles set{sm.bits, in.kg != nullptr, first, last, in.Nk / kTile};
+        first = set.end();
+        if (set.grouped) {
+            __syncthreads();  // the bits of the tiles before are read
+            scan_tiles<false>(sm.bits, own, true, in.kg, (int64_t)b * in.Nk, in.Nk, set.first,
+                              last);
+        }
+        int tile = set.next(set.first), stage = 0;
         if (tile < last) load_keys<HP, kBias>(sm, stage, in, copy, b, tile);
         while (tile < last) {
-            const int ahead = next_tile(sm.bits, tile + 1, first, last);
+            const int ahead = set.next(tile + 1);
             if (ahead < last) {
                 load_keys<HP, kBias>(sm, stage ^ 1, in, copy, b, ahead);
                 cp_wait<1>();
@@ -230,8 +235,7 @@ __device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardAr
                 cp_wait<0>();
             }
             __syncthreads();
-            const bool clear =
-                (sm.bits.clear[(tile - first) >> 5] >> ((tile - first) & 31)) & 1;
+            const bool clear = set.clear(tile);
 #pragma unroll
             for (int st = 0; st < kTile / kHalf; ++st) {
                 float2 dist[4][2];
@@ -392,14 +396,19 @@ __device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const Backwar
                             a.go + ((int64_t)b * in.Nq * in.H + h) * kDim, (int64_t)in.H * kDim,
                             in.Nq);
     const int tiles = a.q_tiles;
-    for (int first = 0; first < tiles; first += kScan) {
-        __syncthreads();
-        scan_tiles<true>(sm.bits, own, own_rows == kRows, in.qg, (int64_t)b * in.Nq, in.Nq, first,
-                         tiles);
-        int tile = next_tile(sm.bits, first, first, tiles), stage = 0;
+    for (int first = 0; first < tiles;) {
+        const Tiles set{sm.bits, in.qg != nullptr, first, tiles,
+                        own_rows == kRows ? in.Nq / kTile : 0};
+        first = set.end();
+        if (set.grouped) {
+            __syncthreads();
+            scan_tiles<true>(sm.bits, own, own_rows == kRows, in.qg, (int64_t)b * in.Nq, in.Nq,
+                             set.first, tiles);
+        }
+        int tile = set.next(set.first), stage = 0;
         if (tile < tiles) load_queries<HP, kBias>(sm, stage, a, copy, b, h, tile);
         while (tile < tiles) {
-            const int ahead = next_tile(sm.bits, tile + 1, first, tiles);
+            const int ahead = set.next(tile + 1);
             if (ahead < tiles) {
                 load_queries<HP, kBias>(sm, stage ^ 1, a, copy, b, h, ahead);
                 cp_wait<1>();
@@ -407,7 +416,7 @@ __device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const Backwar
                 cp_wait<0>();
             }
             __syncthreads();
-            const bool clear = (sm.bits.clear[(tile - first) >> 5] >> ((tile - first) & 31)) & 1;
+            const bool clear = set.clear(tile);
 #pragma unroll
             for (int st = 0; st < kTile / kHalf; ++st) {
                 float2 dist[4][2];
