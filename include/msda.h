@@ -647,12 +647,8 @@ typedef struct {
  *   lse [B, H, Nq]      fp32, written; for the backward (NULL: not wanted)
  * The products are exact and accumulate in fp32, softmax and sums are fp32;
  * the weights are rounded to bf16 for their product with v.  q, k, v and out
- * 16-byte aligned, points 8-byte; workspace >=
- * msda_query_attention_workspace_size(p) bytes (which looks at B, Nq, Nk, H
- * and whether there is a tau), 256-byte aligned, contents ignored. */
-size_t msda_query_attention_workspace_size(const msda_attention_t* p);
+ * 16-byte aligned, points 8-byte. */
 msda_status_t msda_query_attention(const msda_attention_t* p, void* out, float* lse,
-                                   void* workspace, size_t workspace_bytes,
                                    msda_stream_t stream);
 
 /* The derivative of msda_query_attention.  With p_ij = exp(s_ij - lse_i),
@@ -667,8 +663,8 @@ msda_status_t msda_query_attention(const msda_attention_t* p, void* out, float* 
  *   written; grad_tau [B, Nq, H] fp32, written (NULL where p->tau is)
  * p and ds are rounded to bf16 for the products with grad_out, k and q; the
  * sum over j of p dp is formed in fp32 from the unrounded values.  Alignment
- * and workspace as in the forward, with
- * msda_query_attention_backward_workspace_size(p). */
+ * as in the forward; workspace >= msda_query_attention_backward_workspace_size(p)
+ * bytes (which looks at B, Nq and H), 256-byte aligned, contents ignored. */
 size_t msda_query_attention_backward_workspace_size(const msda_attention_t* p);
 msda_status_t msda_query_attention_backward(const msda_attention_t* p, const float* lse,
                                             const void* grad_out, void* grad_q, void* grad_k,

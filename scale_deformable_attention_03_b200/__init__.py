@@ -171,9 +171,7 @@ def lib():
                                                ctypes.c_size_t, _vp]
         L.msda_group_norm_backward.restype = ctypes.c_int
         ap = ctypes.POINTER(Attention)
-        L.msda_query_attention_workspace_size.argtypes = [ap]
-        L.msda_query_attention_workspace_size.restype = ctypes.c_size_t
-        L.msda_query_attention.argtypes = [ap, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+        L.msda_query_attention.argtypes = [ap, _vp, _vp, _vp]
         L.msda_query_attention.restype = ctypes.c_int
         L.msda_query_attention_backward_workspace_size.argtypes = [ap]
         L.msda_query_attention_backward_workspace_size.restype = ctypes.c_size_t
@@ -975,8 +973,7 @@ def _attention_args(name, q, k, v, q_points, k_points, tau, q_group, k_group, sc
 
 
 def msda_query_attention(q, k, v, q_points=None, k_points=None, tau=None, q_group=None,
-                         k_group=None, scale=None, out=None, lse=None, workspace=None,
-                         stream=None):
+                         k_group=None, scale=None, out=None, lse=None, stream=None):
     """Attention of the queries q [B, Nq, H, 32] to k and v [B, Nk, H, 32]
     (bf16; rows may be slices of a wider projection), the scores lowered by
     tau [B, Nq, H] times the distance of q_points [B, Nq, 2] and k_points
@@ -986,16 +983,11 @@ def msda_query_attention(q, k, v, q_points=None, k_points=None, tau=None, q_grou
     torch = _torch()
     name = "msda_query_attention"
     p = _attention_args(name, q, k, v, q_points, k_points, tau, q_group, k_group, scale)
-    with _scope(torch, name, stream, q, k, v, q_points, k_points, tau, q_group, k_group, out, lse,
-                workspace):
+    with _scope(torch, name, stream, q, k, v, q_points, k_points, tau, q_group, k_group, out, lse):
         out = _out(name, out, (p.B, p.Nq, p.H * HEAD_DIM), (torch.bfloat16,), "out", q)
         lse = _out(name, lse, (p.B, p.H, p.Nq), (torch.float32,), "lse", q)
-        need = int(lib().msda_query_attention_workspace_size(p))
-        if need:
-            workspace = _workspace(need, q.device, workspace)
-        _check(lib().msda_query_attention(p, _address(out), _address(lse), _address(workspace),
-                                          workspace.numel() if workspace is not None else 0,
-                                          _raw_stream(torch, q)), name)
+        _check(lib().msda_query_attention(p, _address(out), _address(lse), _raw_stream(torch, q)),
+               name)
     return out, lse
 
 

@@ -6,8 +6,8 @@
 // bias) two heads, so that a distance serves both; its keys come in tiles of
 // 64 through a ring of asynchronous copies.  Tiles that no query of the CTA
 // sees are skipped, tiles without a masked pair take no comparison.  Where the
-// queries do not fill the GPU evenly the keys are split over CTAs, whose sums a
-// second kernel joins.
+// queries do not fill the GPU evenly the keys are split over the CTAs of a
+// cluster, which join their sums through distributed shared memory.
 //
 // With 32 channels per head the products are not what binds: a score costs 64
 // multiply-adds, but also an exponential, and a square root per pair of points
@@ -20,8 +20,6 @@ namespace msda {
 namespace attn {
 namespace {
 
-constexpr int kSms = 148;
-constexpr int kMaxSplits = 64;
 constexpr int kBlocks = 4;  // CTAs per SM: 128 registers a thread (573 us for the 100 x 100 grid, 603 us with 3)
 constexpr int kStages = 3;  // tiles in shared memory
 constexpr int kPart = 32;   // keys per step: scores and distances in registers
@@ -30,11 +28,14 @@ struct ForwardArgs {
     Inputs in;
     __nv_bfloat16* out;
     float* lse;
-    // split keys: per split [B, H, Nq, 32] sums and [B, H, Nq] (maximum, sum)
-    float* part;
-    float2* part_ml;
     int splits, split_tiles, q_tiles;
 };
+
+// Tiles that a CTA keeps where splits only even out the last wave (18 tiles in
+// three parts: 37 us for the first pass of the gradient of 1100 queries, 29 us
+// in one; 79 tiles in two: 166 us for 5000 queries, 181 us in one).
+constexpr int kEvenTiles = 32;
+constexpr int kPartRow = 36;  // floats of a row of split sums, padded for the banks
 
 template <int HP>
 struct ForwardSmem {
@@ -65,12 +66,11 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocks)
     extern __shared__ __align__(128) unsigned char smem[];
     ForwardSmem<HP>& sm = *reinterpret_cast<ForwardSmem<HP>*>(smem);
     const Inputs& in = a.in;
-    int id = blockIdx.x;
+    const int split = blockIdx.x % a.splits;  // its place in the cluster
+    int id = blockIdx.x / a.splits;
     const int qt = id % a.q_tiles;
     id /= a.q_tiles;
-    const int hg = id % (in.H / HP);
-    id /= in.H / HP;
-    const int b = id % in.B, split = id / in.B;
+    const int hg = id % (in.H / HP), b = id / (in.H / HP);
     const int h = hg * HP, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int row = qt * kRows + warp * 16 + g;  // and row + 8
@@ -273,6 +273,11 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocks)
         }
     }
 
+    // split keys: a row's sums, and their reference and sum of weights
+    float* part = reinterpret_cast<float*>(smem);
+    float2* part_ml = reinterpret_cast<float2*>(part + HP * kRows * kPartRow);
+    static_assert(HP * kRows * (kPartRow + 2) * sizeof(float) <= sizeof(sm.k) + sizeof(sm.v), "");
+    if (a.splits > 1) __syncthreads();  // the tiles have been read
 #pragma unroll
     for (int hh = 0; hh < HP; ++hh) {
 #pragma unroll
@@ -280,104 +285,91 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocks)
             float sum = l[hh][half].x + l[hh][half].y;
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            if (!(half ? on1 : on0)) continue;
             const int q = row + 8 * half;
             // a padding query saw the keys of group 0: it is left out here
             const bool dead = sum == 0.0f || (half ? g1 : g0) < 0;
-            const int64_t bhq = ((int64_t)b * in.H + h + hh) * in.Nq + q;
-            if (a.splits == 1) {
-                const float w = dead ? 0.0f : 1.0f / sum;
-                uint32_t* dst = reinterpret_cast<uint32_t*>(
-                    a.out + (((int64_t)b * in.Nq + q) * in.H + h + hh) * kDim);
-#pragma unroll
-                for (int d = 0; d < 4; ++d)
-                    dst[4 * d + t] = dead ? 0u : pack_bf16(o[hh][d][2 * half] * w,
-                                                           o[hh][d][2 * half + 1] * w);
-                if (a.lse != nullptr && t == 0)
-                    a.lse[bhq] = dead ? -INFINITY : (base[hh][half] + log2f(sum)) * kLn2;
-            } else {
-                const int64_t at = (int64_t)split * in.B * in.H * in.Nq + bhq;
-                float2* dst = reinterpret_cast<float2*>(a.part + at * kDim);
+            if (a.splits > 1) {
+                const int r = hh * kRows + warp * 16 + g + 8 * half;
+                float2* dst = reinterpret_cast<float2*>(part + r * kPartRow);
 #pragma unroll
                 for (int d = 0; d < 4; ++d)
                     dst[4 * d + t] = make_float2(o[hh][d][2 * half], o[hh][d][2 * half + 1]);
                 if (t == 0)
-                    a.part_ml[at] = dead ? make_float2(-INFINITY, 0.0f)
-                                         : make_float2(base[hh][half], sum);
+                    part_ml[r] = dead ? make_float2(-INFINITY, 0.0f)
+                                      : make_float2(base[hh][half], sum);
+                continue;
             }
+            if (!(half ? on1 : on0)) continue;
+            const float w = dead ? 0.0f : 1.0f / sum;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(
+                a.out + (((int64_t)b * in.Nq + q) * in.H + h + hh) * kDim);
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                dst[4 * d + t] =
+                    dead ? 0u : pack_bf16(o[hh][d][2 * half] * w, o[hh][d][2 * half + 1] * w);
+            if (a.lse != nullptr && t == 0)
+                a.lse[((int64_t)b * in.H + h + hh) * in.Nq + q] =
+                    dead ? -INFINITY : (base[hh][half] + log2f(sum)) * kLn2;
         }
     }
+    if (a.splits == 1) return;
+    // Each CTA joins every splits-th 16 rows, eight lanes and four channels a row.
+    cluster_sync();
+    const int c = threadIdx.x & 7;
+    for (int r = split * 16 + (int)(threadIdx.x >> 3); r < HP * kRows; r += 16 * a.splits) {
+        const int q = qt * kRows + r % kRows, hh = h + r / kRows;
+        if (q >= in.Nq) continue;
+        const uint32_t at = smem_addr(part + r * kPartRow + 4 * c), at_ml = smem_addr(part_ml + r);
+        float m = -INFINITY;
+        for (int s = 0; s < a.splits; ++s) m = fmaxf(m, remote_f32x2(remote_addr(at_ml, s)).x);
+        float sum = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int s = 0; s < a.splits; ++s) {
+            const float2 ml = remote_f32x2(remote_addr(at_ml, s));
+            const float4 v = remote_f32x4(remote_addr(at, s));
+            if (ml.y == 0.0f) continue;  // nothing seen: the sums may be those of a padding row
+            const float w = exp2_approx(ml.x - m);
+            sum = fmaf(w, ml.y, sum);
+            acc.x = fmaf(w, v.x, acc.x);
+            acc.y = fmaf(w, v.y, acc.y);
+            acc.z = fmaf(w, v.z, acc.z);
+            acc.w = fmaf(w, v.w, acc.w);
+        }
+        const float w = sum == 0.0f ? 0.0f : 1.0f / sum;
+        *reinterpret_cast<uint2*>(a.out + (((int64_t)b * in.Nq + q) * in.H + hh) * kDim + c * 4) =
+            make_uint2(pack_bf16(acc.x * w, acc.y * w), pack_bf16(acc.z * w, acc.w * w));
+        if (a.lse != nullptr && c == 0)
+            a.lse[((int64_t)b * in.H + hh) * in.Nq + q] =
+                sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
+    }
+    cluster_sync();  // nobody's shared memory goes while others read it
 }
 
-// Eight lanes per (item, head, query), four channels each; with kShares = 4 a
-// whole warp, each eight lanes a share of the splits (one query over 33 splits:
-// 4.1 us, against 8.2 us with one share; 900 queries over 3: 5.7 and 3.2 us).
-template <int kShares>
-__global__ void __launch_bounds__(256) attention_join_kernel(const ForwardArgs a)
+template <int HP, bool kBias>
+cudaError_t run(const ForwardArgs& a, cudaStream_t s)
 {
-    const Inputs& in = a.in;
-    const int64_t n = (int64_t)in.B * in.H * in.Nq;
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / (8 * kShares);
-    const int c = threadIdx.x & 7, share = threadIdx.x / 8 % kShares;
-    pdl_wait();
-    if (i >= n) return;
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int s = share; s < a.splits; s += kShares) m = fmaxf(m, a.part_ml[s * n + i].x);
-#pragma unroll
-    for (int x = 8; x < 8 * kShares; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    float l = 0.0f, o[4] = {};
-#pragma unroll 4
-    for (int s = share; s < a.splits; s += kShares) {
-        const float2 ml = a.part_ml[s * n + i];
-        const float4 v = reinterpret_cast<const float4*>(a.part)[(s * n + i) * 8 + c];
-        if (ml.y == 0.0f) continue;  // nothing seen: the sums may be those of a padding row
-        const float w = exp2_approx(ml.x - m);
-        l = fmaf(w, ml.y, l);
-        o[0] = fmaf(w, v.x, o[0]);
-        o[1] = fmaf(w, v.y, o[1]);
-        o[2] = fmaf(w, v.z, o[2]);
-        o[3] = fmaf(w, v.w, o[3]);
-    }
-#pragma unroll
-    for (int x = 8; x < 8 * kShares; x <<= 1) {
-        l += __shfl_xor_sync(0xffffffffu, l, x);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] += __shfl_xor_sync(0xffffffffu, o[k], x);
-    }
-    if (share != 0) return;
-    const float w = l == 0.0f ? 0.0f : 1.0f / l;
-    const int q = (int)(i % in.Nq);
-    const int64_t bh = i / in.Nq;
-    const int64_t at = ((bh / in.H * in.Nq + q) * in.H + bh % in.H) * kDim + c * 4;
-    *reinterpret_cast<uint2*>(a.out + at) =
-        make_uint2(pack_bf16(o[0] * w, o[1] * w), pack_bf16(o[2] * w, o[3] * w));
-    if (a.lse != nullptr && c == 0) a.lse[i] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+    const cudaError_t e = allow_shared<attention_forward_kernel<HP, kBias>>(sizeof(ForwardSmem<HP>));
+    if (e != cudaSuccess) return e;
+    const int64_t ctas = (int64_t)a.q_tiles * a.in.B * (a.in.H / HP) * a.splits;
+    return launch_clusters(attention_forward_kernel<HP, kBias>, a.splits, dim3((unsigned)ctas),
+                           dim3(kAttnThreads), sizeof(ForwardSmem<HP>), s, a);
 }
 
-struct Plan {
-    int q_tiles, splits, split_tiles, heads;  // heads per CTA
-};
+}  // namespace
 
-// Two heads per CTA share the distances, where that still fills the GPU (below
-// it more and shorter CTAs are faster).  The keys are split until the CTAs fill
-// one wave, down to two tiles per CTA (a join costs about what two tiles do),
-// and beyond that where it evens out the last wave: 628 CTAs in waves of 444
-// take two of them, halved they take three half as long.
-Plan plan_of(int B, int Nq, int Nk, int H, bool bias)
+Plan plan_of(int B, int Nq, int Nk, int H, bool bias, int blocks)
 {
     Plan p;
-    p.q_tiles = (Nq + kRows - 1) / kRows;
-    const int64_t wave = kBlocks * kSms;
+    const int64_t wave = blocks * kSms;
     const int tiles = (Nk + kTile - 1) / kTile;
-    int64_t ctas = (int64_t)p.q_tiles * B * H;
+    int64_t ctas = (int64_t)((Nq + kRows - 1) / kRows) * B * H;
     p.heads = bias && H % 2 == 0 && ctas >= 2 * wave ? 2 : 1;
     ctas /= p.heads;
     int64_t splits = wave / std::max<int64_t>(ctas, 1);
     if (splits <= 1) {
         // waves in units of a whole one, 2 % of a wave for each split's join
         double least = 1e30;
-        for (int s = 1; s <= 4; ++s) {
+        for (int s = 1; s == 1 || (s <= 4 && tiles / s >= kEvenTiles); ++s) {
             const double cost = (double)((ctas * s + wave - 1) / wave) / s + 0.02 * (s - 1);
             if (cost < least) {
                 least = cost;
@@ -390,21 +382,6 @@ Plan plan_of(int B, int Nq, int Nk, int H, bool bias)
     p.splits = std::max(1, (tiles + p.split_tiles - 1) / p.split_tiles);
     return p;
 }
-
-template <int HP, bool kBias>
-cudaError_t run(const ForwardArgs& a, cudaStream_t s)
-{
-    const cudaError_t e = allow_shared<attention_forward_kernel<HP, kBias>>(sizeof(ForwardSmem<HP>));
-    if (e != cudaSuccess) return e;
-    const int64_t ctas = (int64_t)a.q_tiles * a.in.B * (a.in.H / HP) * a.splits;
-    attention_forward_kernel<HP, kBias>
-        <<<(unsigned)ctas, kAttnThreads, sizeof(ForwardSmem<HP>), s>>>(a);
-    return cudaGetLastError();
-}
-
-size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
-
-}  // namespace
 
 Inputs inputs_of(const msda_attention_t& p)
 {
@@ -506,17 +483,7 @@ msda_status_t check_workspace(const void* ws, size_t have, size_t need)
 using namespace msda;
 using namespace msda::attn;
 
-extern "C" size_t msda_query_attention_workspace_size(const msda_attention_t* p)
-{
-    if (p == nullptr || p->B <= 0 || p->Nq <= 0 || p->Nk <= 0 || p->H < 1) return 0;
-    const Plan plan = plan_of(p->B, p->Nq, p->Nk, p->H, p->tau != nullptr);
-    if (plan.splits == 1) return 0;
-    const size_t rows = (size_t)plan.splits * p->B * p->H * p->Nq;
-    return up256(rows * kDim * sizeof(float)) + up256(rows * sizeof(float2));
-}
-
 extern "C" msda_status_t msda_query_attention(const msda_attention_t* p, void* out, float* lse,
-                                              void* workspace, size_t workspace_bytes,
                                               msda_stream_t stream)
 {
     bool empty = false;
@@ -530,31 +497,17 @@ extern "C" msda_status_t msda_query_attention(const msda_attention_t* p, void* o
     if (touches_inputs(p, out, (size_t)p->B * p->Nq * p->H * kDim * 2) ||
         touches_inputs(p, lse, (size_t)p->B * p->Nq * p->H * 4))
         return api_fail(MSDA_ERR_INVALID_ARG, "out or lse overlaps q, k or v");
-    const size_t need = msda_query_attention_workspace_size(p);
-    const msda_status_t ws = check_workspace(workspace, workspace_bytes, need);
-    if (ws != MSDA_OK) return ws;
-    const cudaStream_t s = (cudaStream_t)stream;
+    const Plan plan = plan_of(p->B, p->Nq, p->Nk, p->H, p->tau != nullptr, kBlocks);
     ForwardArgs a;
     a.in = inputs_of(*p);
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;
-    const Plan plan = plan_of(p->B, p->Nq, p->Nk, p->H, p->tau != nullptr);
-    a.q_tiles = plan.q_tiles;
+    a.q_tiles = (p->Nq + kRows - 1) / kRows;
     a.splits = plan.splits;
     a.split_tiles = plan.split_tiles;
-    const size_t rows = (size_t)plan.splits * p->B * p->H * p->Nq;
-    a.part = static_cast<float*>(workspace);
-    a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) +
-                                          up256(rows * kDim * sizeof(float)));
-    cudaError_t e = plan.heads == 2 ? run<2, true>(a, s)
+    const cudaStream_t s = (cudaStream_t)stream;
+    return api_cuda(plan.heads == 2 ? run<2, true>(a, s)
                     : p->tau        ? run<1, true>(a, s)
-                                    : run<1, false>(a, s);
-    if (e == cudaSuccess && plan.splits > 1) {
-        const int64_t n = (int64_t)p->B * p->H * p->Nq;
-        const bool many = plan.splits > 8;
-        const int64_t lanes = n * (many ? 32 : 8);
-        e = launch_pdl(many ? attention_join_kernel<4> : attention_join_kernel<1>,
-                       dim3((unsigned)((lanes + 255) / 256)), dim3(256), 0, s, a);
-    }
-    return api_cuda(e, "msda_query_attention");
+                                    : run<1, false>(a, s),
+                    "msda_query_attention");
 }

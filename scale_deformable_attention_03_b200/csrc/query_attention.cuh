@@ -386,6 +386,65 @@ __device__ __forceinline__ void load_columns(Points& pos, int32_t* group, const 
         cp_async<4>(smem_addr(group + threadIdx.x), on ? groups + first + row : groups, on);
 }
 
+// The barrier of a cluster: what its CTAs wrote to shared memory before is seen
+// by all of them after.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile(
+        "barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::
+            : "memory");
+}
+
+// The address of the word at `addr` of this CTA's shared memory in CTA `rank` of the
+// cluster.
+__device__ __forceinline__ uint32_t remote_addr(uint32_t addr, int rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ float remote_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float2 remote_f32x2(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 remote_f32x4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+constexpr int kMaxSplits = 8;  // CTAs of a cluster, on any GPU with clusters
+constexpr int kSms = 148;
+
+// How many CTAs share the keys of 64 queries, and how many heads a CTA has.
+// Two heads share the distances, where that still fills the GPU (below it more
+// and shorter CTAs are faster).  The keys are split until the CTAs fill a wave,
+// down to two tiles per CTA, and of long rows where it evens out the last wave:
+// 628 CTAs in waves of 592 take two of them (704 us for the 100 x 100 grid),
+// quartered they take five a quarter as long (585 us).
+struct Plan {
+    int heads, splits, split_tiles;
+};
+Plan plan_of(int B, int Nq, int Nk, int H, bool bias, int blocks);
+
 // Device copy of the inputs.
 struct Inputs {
     const __nv_bfloat16 *q, *k, *v;

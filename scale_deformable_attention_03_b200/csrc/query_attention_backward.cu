@@ -3,7 +3,7 @@
 //   dq_i = scale sum_j ds_ij k_j,  dtau_i = -sum_j ds_ij |p_i - p_j|
 //   dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij do_i
 // Every sum has one owner, so no atomic is needed.  A first kernel walks the
-// keys for D (its sums joined by a second where the keys are split), the last
+// keys for D (split over the CTAs of a cluster like the forward), the second
 // has two kinds of CTAs, which run side by side so that neither leaves the GPU
 // half empty at its end: 64 queries and all keys for dq and dtau, 64 keys and
 // all queries for dk and dv.  D is formed from the same p and dp that ds uses
@@ -20,9 +20,7 @@ namespace msda {
 namespace attn {
 namespace {
 
-constexpr int kSms = 148;
 constexpr int kBlocks = 3;  // CTAs per SM: 168 registers a thread
-constexpr int kMaxSplits = 32;
 constexpr int kHalf = 32;  // columns per step: scores, dp and distances in registers
 
 struct BackwardArgs {
@@ -32,7 +30,6 @@ struct BackwardArgs {
     __nv_bfloat16 *dq, *dk, *dv;
     float* dtau;
     float* rows;  // [3, B, H, Nq]: -lse and -tau in units of log 2, D
-    float* part;  // [splits, B, H, Nq]: D's sums where the keys are split
     int q_tiles, k_tiles, splits, split_tiles;
 };
 
@@ -41,6 +38,7 @@ struct BackwardSmem {
     alignas(128) unsigned char a[2][HP * kTileBytes];  // keys, or queries
     alignas(128) unsigned char b[2][HP * kTileBytes];  // values, or the output's gradient
     float rows[2][HP][3][kTile];  // of the queries (keys' kernel): lse, tau, D
+    float dots[HP][kTile];        // D's sums where the keys are split
     Points pos[2];
     int32_t group[2][kTile];
     TileBits bits;
@@ -151,7 +149,7 @@ __device__ __forceinline__ float quad_sum(float x)
 // kernel needs of the queries beside it), or with kGrad, given D, dq and dtau.
 template <int HP, bool kBias, bool kGrad>
 __device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardArgs& a, int id,
-                                          int begin, int last, float* sums)
+                                          int split)
 {
     const Inputs& in = a.in;
     const int qt = id % a.q_tiles;
@@ -213,6 +211,8 @@ __device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardAr
                                          8 * half];
     }
 
+    const int begin = kGrad ? 0 : split * a.split_tiles;
+    const int last = kGrad ? a.k_tiles : min(a.k_tiles, begin + a.split_tiles);
     const LaneAt lanes = lane_at(lane);
     const TileCopy<HP> copy(in.k + (int64_t)b * in.Nk * in.ldk + h * kDim, in.ldk,
                             in.v + (int64_t)b * in.Nk * in.ldv + h * kDim, in.ldv, in.Nk);
@@ -326,14 +326,26 @@ __device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardAr
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 D[hh][half] = quad_sum(D[hh][half]);
-                if (t != 0 || !(half ? on1 : on0)) continue;
+                if (t != 0) continue;
+                if (a.splits > 1) sm.dots[hh][warp * 16 + g + 8 * half] = D[hh][half];
+                if (split != 0 || !(half ? on1 : on0)) continue;
                 const int64_t i = ((int64_t)b * in.H + h + hh) * in.Nq + row + 8 * half;
-                sums[i] = D[hh][half];
-                if (begin == 0) {
-                    a.rows[i] = e[hh][half];
-                    a.rows[plane + i] = tau[hh][half];
-                }
+                a.rows[i] = e[hh][half];
+                a.rows[plane + i] = tau[hh][half];
+                if (a.splits == 1) a.rows[2 * plane + i] = D[hh][half];
             }
+        }
+        if (a.splits > 1) {
+            cluster_sync();
+            for (int i = threadIdx.x; split == 0 && i < HP * kTile; i += kAttnThreads) {
+                const int q = qt * kRows + i % kTile;
+                if (q >= in.Nq) continue;
+                float sum = 0.0f;
+                for (int s = 0; s < a.splits; ++s)
+                    sum += remote_f32(remote_addr(smem_addr(&sm.dots[0][i]), s));
+                a.rows[2 * plane + ((int64_t)b * in.H + h + i / kTile) * in.Nq + q] = sum;
+            }
+            cluster_sync();  // nobody's shared memory goes while others read it
         }
     } else {
 #pragma unroll
@@ -489,23 +501,8 @@ template <int HP, bool kBias>
 __global__ void __launch_bounds__(kAttnThreads, kBlocks) attention_dots_kernel(const BackwardArgs a)
 {
     __shared__ BackwardSmem<HP> sm;
-    const int64_t plane = (int64_t)a.in.B * a.in.H * a.in.Nq;
-    const int per = a.q_tiles * (a.in.H / HP) * a.in.B;
-    const int split = blockIdx.x / per, begin = split * a.split_tiles;
-    walk_keys<HP, kBias, false>(sm, a, blockIdx.x - split * per, begin,
-                                min(a.k_tiles, begin + a.split_tiles),
-                                a.splits == 1 ? a.rows + 2 * plane : a.part + split * plane);
-}
-
-__global__ void __launch_bounds__(256) attention_dots_join_kernel(const BackwardArgs a)
-{
-    const int64_t plane = (int64_t)a.in.B * a.in.H * a.in.Nq;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    pdl_wait();
-    if (i >= plane) return;
-    float sum = 0.0f;
-    for (int s = 0; s < a.splits; ++s) sum += a.part[s * plane + i];
-    a.rows[2 * plane + i] = sum;
+    const int id = blockIdx.x / a.splits;
+    walk_keys<HP, kBias, false>(sm, a, id, blockIdx.x - id * a.splits);
 }
 
 template <bool kBias>
@@ -514,38 +511,7 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocks) attention_grad_kernel(c
     __shared__ BackwardSmem<1> sm;
     const int keys = a.k_tiles * a.in.H * a.in.B;  // the longer ones first
     if ((int)blockIdx.x < keys) walk_queries<1, kBias>(sm, a, blockIdx.x);
-    else walk_keys<1, kBias, true>(sm, a, blockIdx.x - keys, 0, a.k_tiles, nullptr);
-}
-
-// CTAs of the first kernel: as in the forward, the keys are split until they
-// fill a wave, and where halves or thirds even out the last one.
-struct Plan {
-    int heads, splits, split_tiles;
-};
-
-Plan plan_of(int B, int Nq, int Nk, int H, bool bias)
-{
-    Plan p;
-    const int64_t wave = kBlocks * kSms;
-    const int tiles = (Nk + kTile - 1) / kTile;
-    int64_t ctas = (int64_t)((Nq + kTile - 1) / kTile) * B * H;
-    p.heads = bias && H % 2 == 0 && ctas >= 2 * wave ? 2 : 1;
-    ctas /= p.heads;
-    int64_t splits = wave / std::max<int64_t>(ctas, 1);
-    if (splits <= 1) {
-        double least = 1e30;
-        for (int s = 1; s <= 4; ++s) {
-            const double cost = (double)((ctas * s + wave - 1) / wave) / s + 0.02 * (s - 1);
-            if (cost < least) {
-                least = cost;
-                splits = s;
-            }
-        }
-    }
-    splits = std::max<int64_t>(1, std::min<int64_t>({splits, (tiles + 1) / 2, kMaxSplits}));
-    p.split_tiles = std::max<int>(1, (tiles + (int)splits - 1) / (int)splits);
-    p.splits = std::max(1, (tiles + p.split_tiles - 1) / p.split_tiles);
-    return p;
+    else walk_keys<1, kBias, true>(sm, a, blockIdx.x - keys, 0);
 }
 
 cudaError_t run(const BackwardArgs& a, const Plan& plan, bool bias, cudaStream_t s)
@@ -554,13 +520,10 @@ cudaError_t run(const BackwardArgs& a, const Plan& plan, bool bias, cudaStream_t
     cudaError_t e = cudaSuccess;
     if (a.in.Nq > 0) {
         const unsigned ctas = (unsigned)(items / plan.heads * a.q_tiles * a.splits);
-        if (plan.heads == 2) attention_dots_kernel<2, true><<<ctas, kAttnThreads, 0, s>>>(a);
-        else if (bias) attention_dots_kernel<1, true><<<ctas, kAttnThreads, 0, s>>>(a);
-        else attention_dots_kernel<1, false><<<ctas, kAttnThreads, 0, s>>>(a);
-        e = cudaGetLastError();
-        if (e == cudaSuccess && a.splits > 1)
-            e = launch_pdl(attention_dots_join_kernel,
-                           dim3((unsigned)((items * a.in.Nq + 255) / 256)), dim3(256), 0, s, a);
+        const auto kernel = plan.heads == 2 ? attention_dots_kernel<2, true>
+                            : bias          ? attention_dots_kernel<1, true>
+                                            : attention_dots_kernel<1, false>;
+        e = launch_clusters(kernel, a.splits, dim3(ctas), dim3(kAttnThreads), 0, s, a);
         if (e != cudaSuccess) return e;
     }
     const unsigned ctas = (unsigned)(items * (a.q_tiles + a.k_tiles));
@@ -579,8 +542,7 @@ using namespace msda::attn;
 extern "C" size_t msda_query_attention_backward_workspace_size(const msda_attention_t* p)
 {
     if (p == nullptr || p->B <= 0 || p->Nq <= 0 || p->H < 1) return 0;
-    const Plan plan = plan_of(p->B, p->Nq, p->Nk, p->H, p->tau != nullptr);
-    return (size_t)(3 + (plan.splits > 1 ? plan.splits : 0)) * sizeof(float) * p->B * p->H * p->Nq;
+    return 3 * sizeof(float) * (size_t)p->B * p->H * p->Nq;
 }
 
 extern "C" msda_status_t msda_query_attention_backward(const msda_attention_t* p, const float* lse,
@@ -622,9 +584,8 @@ extern "C" msda_status_t msda_query_attention_backward(const msda_attention_t* p
     a.dk = static_cast<__nv_bfloat16*>(grad_k);
     a.dv = static_cast<__nv_bfloat16*>(grad_v);
     a.dtau = grad_tau;
-    const Plan plan = plan_of(p->B, p->Nq, p->Nk, p->H, p->tau != nullptr);
+    const Plan plan = plan_of(p->B, p->Nq, p->Nk, p->H, p->tau != nullptr, kBlocks);
     a.rows = static_cast<float*>(workspace);
-    a.part = a.rows + 3 * rows_q;
     a.splits = plan.splits;
     a.split_tiles = plan.split_tiles;
     a.q_tiles = (p->Nq + kTile - 1) / kTile;

@@ -248,12 +248,10 @@ def test_same_bits_streams_and_capture():
     s.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(first, (o2, l2) + g2))
     p = msda.Attention(B=2, Nq=333, Nk=333, H=8)
-    size = max(msda.lib().msda_query_attention_workspace_size(p),
-               msda.lib().msda_query_attention_backward_workspace_size(p))
-    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(msda.lib().msda_query_attention_backward_workspace_size(p), dtype=torch.uint8, device="cuda")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        msda.msda_query_attention(**a, out=out, lse=lse, workspace=ws)
+        msda.msda_query_attention(**a, out=out, lse=lse)
         msda.msda_query_attention_backward(**a, lse=lse, grad_out=do, out=grads, workspace=ws)
     for t in (out, lse) + grads:
         t.zero_()

@@ -173,8 +173,8 @@ def _attention(**kw):
     return msda.Attention(**a)
 
 
-def _attend(L, p, out=FAKE + (3 << 24), lse=FAKE + (4 << 24), ws=FAKE + (1 << 30), n=1 << 30):
-    return L.msda_query_attention(p, out, lse, ws, n, None)
+def _attend(L, p, out=FAKE + (3 << 24), lse=FAKE + (4 << 24)):
+    return L.msda_query_attention(p, out, lse, None)
 
 
 def _attend_back(L, p, lse=FAKE + (4 << 24), go=FAKE + (5 << 24), gq=FAKE + (6 << 24),
@@ -212,22 +212,21 @@ def test_attention_rejects_bad_inputs(L, kw, code, fragment):
     for call in (_attend, _attend_back):
         assert call(L, _attention(**kw)) == code
         assert fragment in L.msda_last_error().decode()
-    assert L.msda_query_attention(None, FAKE, FAKE, FAKE, 1 << 20, None) == INVALID
+    assert L.msda_query_attention(None, FAKE, FAKE, None) == INVALID
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(out=None), INVALID), (dict(out=FAKE + 8), INVALID), (dict(lse=FAKE + 2), INVALID),
-    (dict(out=FAKE), INVALID), (dict(out=FAKE + (2 << 24) + 64), INVALID),
-    (dict(ws=None), WORKSPACE), (dict(ws=FAKE + 16), WORKSPACE), (dict(n=100), WORKSPACE)])
+    (dict(out=FAKE), INVALID), (dict(out=FAKE + (2 << 24) + 64), INVALID)])
 def test_attention_rejects_bad_outputs(L, kw, code):
-    assert L.msda_query_attention_workspace_size(_attention()) > 0   # keys are split here
     assert _attend(L, _attention(), **kw) == code
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(lse=None), INVALID), (dict(go=None), INVALID), (dict(gq=None), INVALID),
     (dict(gk=None), INVALID), (dict(gv=FAKE + 8), INVALID), (dict(gt=None), INVALID),
-    (dict(gk=FAKE), INVALID), (dict(ws=None), WORKSPACE), (dict(n=8), WORKSPACE)])
+    (dict(gk=FAKE), INVALID), (dict(ws=None), WORKSPACE), (dict(ws=FAKE + 16), WORKSPACE),
+    (dict(n=8), WORKSPACE)])
 def test_attention_backward_rejects_bad_outputs(L, kw, code):
     p = _attention(q_points=FAKE, k_points=FAKE, tau=FAKE)
     assert _attend_back(L, p, **kw) == code
@@ -235,6 +234,6 @@ def test_attention_backward_rejects_bad_outputs(L, kw, code):
 
 def test_attention_of_nothing(L):
     for kw in (dict(B=0), dict(Nq=0)):
-        assert _attend(L, _attention(**kw, q=None), out=None, lse=None, ws=None, n=0) == OK
+        assert _attend(L, _attention(**kw, q=None), out=None, lse=None) == OK
     assert _attend_back(L, _attention(B=0, q=None, k=None, v=None), lse=None, go=None, gq=None,
                         gk=None, gv=None, ws=None, n=0) == OK
