@@ -22,6 +22,9 @@
 // and then walks its run backwards: what the first pass read last is still in
 // L2 (126 MB).  It is a programmatic dependent of the first.
 //
+// A few rows take one launch: a cluster of up to eight CTAs does both passes,
+// with its barrier in between.
+//
 // Bound by memory: the rows are read twice, the second time from L2 as far as
 // that reaches, and written once.
 #include <cuda_bf16.h>
@@ -41,11 +44,14 @@ constexpr int kNormWarps = kNormThreads / 32;
 constexpr int kMaxC = MSDA_NORM_MAX_CHANNELS;
 constexpr int kSms = 148;
 constexpr int kMaxRuns = 2 * kSms;  // two CTAs per SM
+constexpr int kCluster = 8;         // CTAs of the one-launch form (375 rows: 25.3 us a call, 28.4 us with two launches),
+constexpr int kSmallRows = 8;       // which takes up to 8 rows per thread
 
 struct NormShape {
     int B, Nv, C, L, G, cg;  // cg = C / G
     int tpr, slots;          // threads per row, rows side by side
     int runs;                // CTAs that share the rows
+    bool small;              // and form one cluster
     int used;                // rows of an item in its levels, cum[L]
     int start[kMaxLevels], cum[kMaxLevels + 1];
     int gaps;                // runs of rows in no level
@@ -394,16 +400,17 @@ __device__ __forceinline__ double add_lanes(double v, int seg)
 // cancels.  Within a channel the sums are fp32 and relative to the channel's
 // own value in that row; they are moved to m and added over the channels in
 // double.
+struct SumsSmem {
+    alignas(16) float s[2 * kNormThreads * 8];
+    float first[kMaxC];
+};
+
 template <bool kX>
-__global__ void __launch_bounds__(kNormThreads, 2) norm_stats_kernel(const void* __restrict__ x,
-                                                                     const NormShape n,
-                                                                     double2* __restrict__ part,
-                                                                     double* __restrict__ middle)
+__device__ __forceinline__ void norm_stats(SumsSmem& sm, const void* __restrict__ x,
+                                           const NormShape& n, double2* part, double* middle)
 {
     constexpr bool kSplit = !kX;
-    __shared__ __align__(16) float s[2 * kNormThreads * 8];
-    __shared__ float first[kMaxC];
-    pdl_trigger();
+    float *s = sm.s, *first = sm.first;
     const int slot = threadIdx.x / n.tpr;
     const Quads c = quads_of<kSplit>(n.C, threadIdx.x - slot * n.tpr);
     const GroupLanes gl = group_lanes(n.cg);
@@ -528,18 +535,30 @@ __device__ void zero_gaps(const NormShape& n, void* y, int cta, int ctas)
     }
 }
 
-template <bool kX, bool kY, int kAct>
-__global__ void __launch_bounds__(kNormThreads, 2) norm_apply_kernel(
-    const void* __restrict__ x, const NormShape n, const double2* __restrict__ part,
-    const double* __restrict__ middle, float eps,
-    const float* __restrict__ gamma, const float* __restrict__ beta, void* __restrict__ y,
-    float* __restrict__ mean_out, float* __restrict__ rstd_out)
+struct ApplySmem {
+    Shares shares;
+    // the mean as two floats: what is subtracted is exact to 48 bits, whatever the mean
+    float hi[kMaxC], lo[kMaxC], r[kMaxC];
+};
+
+struct NormOut {
+    float eps;
+    const float *gamma, *beta;
+    void* y;
+    float *mean, *rstd;
+};
+
+// The rows of a run, last ones first; `ready` is called before anything that the
+// first pass wrote is read.
+template <bool kX, bool kY, int kAct, typename Ready>
+__device__ __forceinline__ void norm_apply(ApplySmem& sm, const void* __restrict__ x,
+                                           const NormShape& n, const double2* part,
+                                           const double* middle, const NormOut& out, int run,
+                                           Ready ready)
 {
     constexpr bool kSplit = !(kX && kY);
-    __shared__ Shares shares;
-    // the mean as two floats: what is subtracted is exact to 48 bits, whatever the mean
-    __shared__ float st_hi[kMaxC], st_lo[kMaxC], st_r[kMaxC];
-    const int run = n.runs - 1 - (int)blockIdx.x;
+    Shares& shares = sm.shares;
+    float *st_hi = sm.hi, *st_lo = sm.lo, *st_r = sm.r;
     const int slot = threadIdx.x / n.tpr;
     const Quads c = quads_of<kSplit>(n.C, threadIdx.x - slot * n.tpr);
     const int64_t begin = run_begin(n, run);
@@ -555,7 +574,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_apply_kernel(
             -(int64_t)n.slots * n.C,
             slot < n.slots ? (sp.rows - slot + n.slots - 1) / n.slots : 0};
         walk.start();
-        if (!waited) pdl_wait();  // nothing that the pass before writes is read above
+        if (!waited) ready();
         waited = true;
         const int64_t bl = (int64_t)sp.b * n.L + sp.l;
         for (int g0 = 0; g0 < n.G; g0 += 32) {
@@ -566,21 +585,21 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_apply_kernel(
                 const double mean = middle[bl * n.G + g] + acc.x / N;
                 double var = (acc.y - acc.x * acc.x / N) / N;
                 if (var < 0.0) var = 0.0;  // rounding only; a NaN stays
-                const float hi = (float)mean, r = (float)(1.0 / sqrt(var + (double)eps));
+                const float hi = (float)mean, r = (float)(1.0 / sqrt(var + (double)out.eps));
                 st_hi[g] = hi;
                 st_lo[g] = (float)(mean - (double)hi);
                 st_r[g] = r;
                 // the run with the level's first row writes the statistics
                 if (begin <= (int64_t)sp.b * n.used + n.cum[sp.l]) {
-                    if (mean_out) mean_out[bl * n.G + g] = hi;
-                    if (rstd_out) rstd_out[bl * n.G + g] = r;
+                    if (out.mean) out.mean[bl * n.G + g] = hi;
+                    if (out.rstd) out.rstd[bl * n.G + g] = r;
                 }
             }
             __syncthreads();
         }
         if (slot < n.slots) {
-            const Vec8 ga = load_channels(gamma, (int64_t)sp.l * n.C, c, 1.0f);
-            const Vec8 be = load_channels(beta, (int64_t)sp.l * n.C, c, 0.0f);
+            const Vec8 ga = load_channels(out.gamma, (int64_t)sp.l * n.C, c, 1.0f);
+            const Vec8 be = load_channels(out.beta, (int64_t)sp.l * n.C, c, 0.0f);
             Vec8 hi, lo, a;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -593,13 +612,51 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_apply_kernel(
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     v.v[j] = activate<kAct>(fmaf((v.v[j] - hi.v[j]) - lo.v[j], a.v[j], be.v[j]));
-                store8<kY, kSplit>(y, at, c, v);
+                store8<kY, kSplit>(out.y, at, c, v);
             });
         }
         end -= sp.rows;
         __syncthreads();  // the statistics are read before the next span's are written
     }
-    zero_gaps<kY>(n, y, blockIdx.x, gridDim.x);
+    zero_gaps<kY>(n, out.y, run, n.runs);
+}
+
+template <bool kX>
+__global__ void __launch_bounds__(kNormThreads, 2) norm_stats_kernel(const void* __restrict__ x,
+                                                                     const NormShape n,
+                                                                     double2* __restrict__ part,
+                                                                     double* __restrict__ middle)
+{
+    __shared__ SumsSmem sm;
+    pdl_trigger();
+    norm_stats<kX>(sm, x, n, part, middle);
+}
+
+template <bool kX, bool kY, int kAct>
+__global__ void __launch_bounds__(kNormThreads, 2) norm_apply_kernel(
+    const void* __restrict__ x, const NormShape n, const double2* __restrict__ part,
+    const double* __restrict__ middle, const NormOut out)
+{
+    __shared__ ApplySmem sm;
+    norm_apply<kX, kY, kAct>(sm, x, n, part, middle, out, n.runs - 1 - (int)blockIdx.x,
+                             [] { pdl_wait(); });
+}
+
+// Both passes, for one cluster; a CTA's own rows come back from its L1 or L2.
+template <bool kX, bool kY, int kAct>
+__global__ void __launch_bounds__(kNormThreads, 2) norm_small_kernel(const void* __restrict__ x,
+                                                                     const NormShape n,
+                                                                     double2* part,
+                                                                     double* middle,
+                                                                     const NormOut out)
+{
+    __shared__ union {
+        SumsSmem sums;
+        ApplySmem apply;
+    } sm;
+    norm_stats<kX>(sm.sums, x, n, part, middle);
+    cluster_sync();
+    norm_apply<kX, kY, kAct>(sm.apply, x, n, part, middle, out, blockIdx.x, [] {});
 }
 
 // --------------------------------------------------------------- backward
@@ -647,16 +704,24 @@ __device__ __forceinline__ Channels load_constants(const NormShape& n, int b, in
 
 // A span's sums of dz and dz xh per channel (fp32, for the parameters'
 // gradients) and, weighted with gamma, per group (double, for dx).
+struct GradIn {
+    const void *x, *dy;
+    const float *mean, *rstd, *gamma, *beta;
+};
+
+struct GradOut {
+    void* dx;
+    float *dgamma, *dbeta;
+};
+
 template <bool kX, bool kDy, int kAct>
-__global__ void __launch_bounds__(kNormThreads, 2) norm_grad_sums_kernel(
-    const void* __restrict__ x, const void* __restrict__ dy, const NormShape n,
-    const float* __restrict__ mean, const float* __restrict__ rstd,
-    const float* __restrict__ gamma, const float* __restrict__ beta, float* __restrict__ chan,
-    double2* __restrict__ part)
+__device__ __forceinline__ void norm_grad_sums(SumsSmem& sm, const GradIn& in, const NormShape& n,
+                                               float* chan, double2* part)
 {
     constexpr bool kSplit = !(kX && kDy);
-    __shared__ __align__(16) float s[2 * kNormThreads * 8];
-    pdl_trigger();
+    const void *__restrict__ x = in.x, *__restrict__ dy = in.dy;
+    const float *mean = in.mean, *rstd = in.rstd, *gamma = in.gamma, *beta = in.beta;
+    float* s = sm.s;
     const int slot = threadIdx.x / n.tpr;
     const Quads c = quads_of<kSplit>(n.C, threadIdx.x - slot * n.tpr);
     const GroupLanes gl = group_lanes(n.cg);
@@ -741,25 +806,32 @@ __device__ __forceinline__ void add_parameters(Shares& sh, const float* chan, co
     }
 }
 
-template <bool kX, bool kDy, bool kDx, int kAct>
-__global__ void __launch_bounds__(kNormThreads, 2) norm_grad_apply_kernel(
-    const void* __restrict__ x, const void* __restrict__ dy, const NormShape n,
-    const float* __restrict__ mean, const float* __restrict__ rstd,
-    const float* __restrict__ gamma, const float* __restrict__ beta,
-    const float* __restrict__ chan, const double2* __restrict__ part, void* __restrict__ dx,
-    float* __restrict__ dgamma, float* __restrict__ dbeta)
+struct GradSmem {
+    Shares shares;
+    float c1[kMaxC], c2[kMaxC];
+};
+
+// Block i of the parameters' gradients: a level's 32 channels.
+__device__ __forceinline__ int parameter_blocks(const NormShape& n) { return n.L * ((n.C + 31) / 32); }
+
+__device__ __forceinline__ void parameter_block(Shares& sh, const float* chan, const NormShape& n,
+                                                int i, const GradOut& out)
+{
+    const int blocks = (n.C + 31) / 32, l = i / blocks;
+    add_parameters(sh, chan, n, l, (i - l * blocks) * 32 + (threadIdx.x & 31), out.dgamma,
+                   out.dbeta);
+}
+
+template <bool kX, bool kDy, bool kDx, int kAct, typename Ready>
+__device__ __forceinline__ void norm_grad_apply(GradSmem& sm, const GradIn& in, const NormShape& n,
+                                                const double2* part, const GradOut& out, int run,
+                                                Ready ready)
 {
     constexpr bool kSplit = !(kX && kDy && kDx);
-    __shared__ Shares shares;
-    __shared__ float c1s[kMaxC], c2s[kMaxC];
-    if ((int)blockIdx.x >= n.runs) {  // the CTAs behind the runs: parameter gradients
-        pdl_wait();
-        const int i = blockIdx.x - n.runs, blocks = (n.C + 31) / 32, l = i / blocks;
-        add_parameters(shares, chan, n, l, (i - l * blocks) * 32 + (threadIdx.x & 31), dgamma,
-                       dbeta);
-        return;
-    }
-    const int run = n.runs - 1 - (int)blockIdx.x;
+    const void *__restrict__ x = in.x, *__restrict__ dy = in.dy;
+    const float *mean = in.mean, *rstd = in.rstd, *gamma = in.gamma, *beta = in.beta;
+    Shares& shares = sm.shares;
+    float *c1s = sm.c1, *c2s = sm.c2;
     const int slot = threadIdx.x / n.tpr;
     const Quads c = quads_of<kSplit>(n.C, threadIdx.x - slot * n.tpr);
     const int64_t begin = run_begin(n, run);
@@ -775,7 +847,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_grad_apply_kernel(
             -(int64_t)n.slots * n.C,
             slot < n.slots ? (sp.rows - slot + n.slots - 1) / n.slots : 0};
         walk.start();
-        if (!waited) pdl_wait();
+        if (!waited) ready();
         waited = true;
         const double inv = 1.0 / ((double)(n.cum[sp.l + 1] - n.cum[sp.l]) * n.cg);
         for (int g0 = 0; g0 < n.G; g0 += 32) {
@@ -807,13 +879,59 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_grad_apply_kernel(
                     const float t = __fmul_rn(k.gamma.v[j], dz);
                     o.v[j] = k.rstd.v[j] * fmaf(-hat, c2.v[j], __fsub_rn(t, c1.v[j]));
                 }
-                store8<kDx, kSplit>(dx, at, c, o);
+                store8<kDx, kSplit>(out.dx, at, c, o);
             });
         }
         end -= sp.rows;
         __syncthreads();
     }
-    zero_gaps<kDx>(n, dx, blockIdx.x, n.runs);
+    zero_gaps<kDx>(n, out.dx, run, n.runs);
+}
+
+template <bool kX, bool kDy, int kAct>
+__global__ void __launch_bounds__(kNormThreads, 2) norm_grad_sums_kernel(
+    const GradIn in, const NormShape n, float* __restrict__ chan, double2* __restrict__ part)
+{
+    __shared__ SumsSmem sm;
+    pdl_trigger();
+    norm_grad_sums<kX, kDy, kAct>(sm, in, n, chan, part);
+}
+
+// The CTAs behind the runs take a block of the parameters' gradients each.
+template <bool kX, bool kDy, bool kDx, int kAct>
+__global__ void __launch_bounds__(kNormThreads, 2) norm_grad_apply_kernel(
+    const GradIn in, const NormShape n, const float* __restrict__ chan,
+    const double2* __restrict__ part, const GradOut out)
+{
+    __shared__ GradSmem sm;
+    const int i = (int)blockIdx.x - n.runs;
+    if (i >= 0) {
+        pdl_wait();
+        parameter_block(sm.shares, chan, n, i, out);
+    } else {
+        norm_grad_apply<kX, kDy, kDx, kAct>(sm, in, n, part, out, -1 - i, [] { pdl_wait(); });
+    }
+}
+
+// Both passes, for one cluster.
+template <bool kX, bool kDy, bool kDx, int kAct>
+__global__ void __launch_bounds__(kNormThreads, 2) norm_grad_small_kernel(const GradIn in,
+                                                                          const NormShape n,
+                                                                          float* chan,
+                                                                          double2* part,
+                                                                          const GradOut out)
+{
+    __shared__ union {
+        SumsSmem sums;
+        GradSmem grad;
+    } sm;
+    norm_grad_sums<kX, kDy, kAct>(sm.sums, in, n, chan, part);
+    cluster_sync();
+    norm_grad_apply<kX, kDy, kDx, kAct>(sm.grad, in, n, part, out, blockIdx.x, [] {});
+    for (int i = blockIdx.x; i < parameter_blocks(n); i += gridDim.x) {
+        __syncthreads();  // the shares are free
+        parameter_block(sm.grad.shares, chan, n, i, out);
+    }
 }
 
 // ------------------------------------------------------------------- host
@@ -890,9 +1008,10 @@ msda_status_t norm_shape(const msda_norm_dims_t& d, const int64_t* shapes, const
     // rows are counted in 48 bits, so that their products with the runs fit 64
     if ((int64_t)d.B * d.Nv > ((int64_t)1 << 48) || (int64_t)d.B * d.L > INT32_MAX)
         return api_fail(MSDA_ERR_UNSUPPORTED, "too many rows");
-    // four rows per thread at least
-    const int64_t least = (int64_t)n.slots * 4;
-    n.runs = (int)std::min<int64_t>(kMaxRuns, ((int64_t)d.B * n.used + least - 1) / least);
+    // four rows per thread at least; up to kSmallRows in one cluster
+    const int64_t rows = (int64_t)d.B * n.used, least = (int64_t)n.slots * 4;
+    n.small = rows <= (int64_t)kCluster * n.slots * kSmallRows;
+    n.runs = (int)std::min<int64_t>(n.small ? kCluster : kMaxRuns, (rows + least - 1) / least);
     return MSDA_OK;
 }
 
@@ -940,26 +1059,30 @@ msda_status_t norm_dtype(msda_dtype_t t, const char* name)
 struct NormArgs {
     const void* x;
     NormShape n;
-    const float *gamma, *beta;
-    float eps;
     double2* part;
     double* middle;
-    void* y;
-    float *mean, *rstd;
+    NormOut out;
 };
 
 template <bool kX, bool kY, int kAct>
 cudaError_t run_forward(const NormArgs& a, cudaStream_t s)
 {
-    cudaError_t e = allow_shared<norm_stats_kernel<kX>>(kRingBytes);
+    const dim3 block(kNormThreads);
+    cudaError_t e;
+    if (a.n.small) {
+        e = allow_shared<norm_small_kernel<kX, kY, kAct>>(kRingBytes);
+        if (e != cudaSuccess) return e;
+        return launch_clusters(norm_small_kernel<kX, kY, kAct>, a.n.runs, dim3(a.n.runs), block,
+                               kRingBytes, s, a.x, a.n, a.part, a.middle, a.out);
+    }
+    e = allow_shared<norm_stats_kernel<kX>>(kRingBytes);
     if (e == cudaSuccess) e = allow_shared<norm_apply_kernel<kX, kY, kAct>>(kRingBytes);
     if (e != cudaSuccess) return e;
-    norm_stats_kernel<kX><<<a.n.runs, kNormThreads, kRingBytes, s>>>(a.x, a.n, a.part,
-                                                                         a.middle);
+    norm_stats_kernel<kX><<<a.n.runs, block, kRingBytes, s>>>(a.x, a.n, a.part, a.middle);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_pdl(norm_apply_kernel<kX, kY, kAct>, dim3(a.n.runs), dim3(kNormThreads),
-                      kRingBytes, s, a.x, a.n, a.part, a.middle, a.eps, a.gamma, a.beta, a.y, a.mean, a.rstd);
+    return launch_pdl(norm_apply_kernel<kX, kY, kAct>, dim3(a.n.runs), block, kRingBytes, s, a.x,
+                      a.n, a.part, a.middle, a.out);
 }
 
 template <bool kX, bool kY>
@@ -971,29 +1094,34 @@ cudaError_t run_forward(const NormArgs& a, msda_activation_t act, cudaStream_t s
 }
 
 struct GradArgs {
-    const void *x, *dy;
+    GradIn in;
     NormShape n;
-    const float *mean, *rstd, *gamma, *beta;
     float* chan;
     double2* part;
-    void* dx;
-    float *dgamma, *dbeta;
+    GradOut out;
 };
 
 template <bool kX, bool kDy, bool kDx, int kAct>
 cudaError_t run_backward(const GradArgs& a, cudaStream_t s)
 {
     const NormShape& n = a.n;
-    cudaError_t e = allow_shared<norm_grad_sums_kernel<kX, kDy, kAct>>(kRingBytes);
+    const dim3 block(kNormThreads);
+    cudaError_t e;
+    if (n.small) {
+        e = allow_shared<norm_grad_small_kernel<kX, kDy, kDx, kAct>>(kRingBytes);
+        if (e != cudaSuccess) return e;
+        return launch_clusters(norm_grad_small_kernel<kX, kDy, kDx, kAct>, n.runs, dim3(n.runs),
+                               block, kRingBytes, s, a.in, n, a.chan, a.part, a.out);
+    }
+    e = allow_shared<norm_grad_sums_kernel<kX, kDy, kAct>>(kRingBytes);
     if (e == cudaSuccess) e = allow_shared<norm_grad_apply_kernel<kX, kDy, kDx, kAct>>(kRingBytes);
     if (e != cudaSuccess) return e;
-    norm_grad_sums_kernel<kX, kDy, kAct><<<n.runs, kNormThreads, kRingBytes, s>>>(
-        a.x, a.dy, n, a.mean, a.rstd, a.gamma, a.beta, a.chan, a.part);
+    norm_grad_sums_kernel<kX, kDy, kAct><<<n.runs, block, kRingBytes, s>>>(a.in, n, a.chan, a.part);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_pdl(norm_grad_apply_kernel<kX, kDy, kDx, kAct>,
-                      dim3(n.runs + n.L * ((n.C + 31) / 32)), dim3(kNormThreads), kRingBytes, s,
-                      a.x, a.dy, n, a.mean, a.rstd, a.gamma, a.beta, a.chan, a.part, a.dx, a.dgamma, a.dbeta);
+                      dim3(n.runs + n.L * ((n.C + 31) / 32)), block, kRingBytes, s, a.in, n,
+                      a.chan, a.part, a.out);
 }
 
 template <bool kX, bool kDy, bool kDx>
@@ -1050,15 +1178,10 @@ extern "C" msda_status_t msda_group_norm(const void* x, msda_dtype_t x_dtype,
         return api_fail(MSDA_ERR_INVALID_ARG, "y overlaps x");
     NORM_TRY(norm_workspace(workspace, workspace_bytes, msda_group_norm_workspace_size(d)));
     a.x = x;
-    a.gamma = gamma;
-    a.beta = beta;
-    a.eps = eps;
     a.part = static_cast<double2*>(workspace);
     a.middle = reinterpret_cast<double*>(static_cast<char*>(workspace) +
                                          up256(sizeof(double2) * norm_max_spans(d) * d.G));
-    a.y = y;
-    a.mean = mean;
-    a.rstd = rstd;
+    a.out = {eps, gamma, beta, y, mean, rstd};
     const auto run = x_dtype == MSDA_BF16
                          ? (y_dtype == MSDA_BF16 ? run_forward<true, true> : run_forward<true, false>)
                          : (y_dtype == MSDA_BF16 ? run_forward<false, true>
@@ -1104,17 +1227,10 @@ extern "C" msda_status_t msda_group_norm_backward(
     NORM_TRY(norm_workspace(workspace, workspace_bytes,
                             msda_group_norm_backward_workspace_size(d)));
     char* w = static_cast<char*>(workspace);
-    a.x = x;
-    a.dy = grad_y;
-    a.mean = mean;
-    a.rstd = rstd;
-    a.gamma = gamma;
-    a.beta = beta;
+    a.in = {x, grad_y, mean, rstd, gamma, beta};
     a.part = reinterpret_cast<double2*>(w);
     a.chan = reinterpret_cast<float*>(w + up256(sizeof(double2) * norm_max_spans(d) * d.G));
-    a.dx = grad_x;
-    a.dgamma = grad_gamma;
-    a.dbeta = grad_beta;
+    a.out = {grad_x, grad_gamma, grad_beta};
     using Run = cudaError_t (*)(const GradArgs&, msda_activation_t, cudaStream_t);
     static constexpr Run runs[8] = {
         run_backward<false, false, false>, run_backward<false, false, true>,

@@ -30,6 +30,15 @@ __device__ __forceinline__ void pdl_trigger()
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// The barrier of a cluster: what its CTAs wrote before, to shared and to global
+// memory, is seen by all of them after.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile(
+        "barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::
+            : "memory");
+}
+
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 constexpr int kHeadDim = 32;

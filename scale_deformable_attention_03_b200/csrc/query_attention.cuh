@@ -386,15 +386,6 @@ __device__ __forceinline__ void load_columns(Points& pos, int32_t* group, const 
         cp_async<4>(smem_addr(group + threadIdx.x), on ? groups + first + row : groups, on);
 }
 
-// The barrier of a cluster: what its CTAs wrote to shared memory before is seen
-// by all of them after.
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile(
-        "barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::
-            : "memory");
-}
-
 // The address of the word at `addr` of this CTA's shared memory in CTA `rank` of the
 // cluster.
 __device__ __forceinline__ uint32_t remote_addr(uint32_t addr, int rank)
