@@ -149,3 +149,95 @@ def test_nothing_is_written_around_the_outputs():
     for flat, t in frames:
         n = t.numel()
         assert bool((flat[:64] == 3).all()) and bool((flat[64 + n:] == 3).all())
+
+
+def test_norm_of_many_small_items():
+    """More spans than CTAs: every run crosses many levels and items."""
+    levels, B = [(1, 1), (1, 2), (2, 1)], 3001
+    x, shapes, starts, gamma, beta = norm.problem(levels, 1, 16, 2, B, torch.float32, 8)
+    y, mean, rstd = msda.msda_group_norm(x, shapes, starts, 2, gamma, beta, activation="silu")
+    want, _, _, core = norm.forward64(x, shapes, starts, 2, gamma, beta, 1e-5, "silu")
+    assert bool(((y.double() - want).abs() <= 2.0 ** -14 * core + 2.0 ** -24 * want.abs()).all())
+    dy = torch.randn(x.shape, device="cuda")
+    gx, gg, gb = msda.msda_group_norm_backward(x, shapes, starts, 2, mean, rstd, dy, gamma, beta, "silu")
+    wx, wg, wb, size, sg, sb = norm.backward64(x, shapes, starts, 2, mean, rstd, dy, gamma, beta, "silu")
+    assert bool(((gx.double() - wx).abs() <= (2.0 ** -18 + 2.0 ** -20) * size + 2.0 ** -24 * wx.abs()).all())
+    assert bool(((gg.double() - wg).abs() <= 2.0 ** -18 * sg + 2.0 ** -24 * wg.abs()).all())
+    assert bool(((gb.double() - wb).abs() <= 2.0 ** -18 * sb + 2.0 ** -24 * wb.abs()).all())
+
+
+def test_offsets_past_32_bits():
+    """Elements behind the 2^31st of each operator's tensors."""
+    # the norm: five items of 2^20 rows of 512, the last one checked.  Its sums are longer than
+    # the small problems': at most 2^20 / 296 * 5 rows a run, four of them side by side, are 4500
+    # additions in fp32; their roundings are of random sign, 6 sqrt(4500) u (1 + D^2) < 2^-11 of
+    # the variance, half of it in r, and 2^-12 of a spread in the mean
+    x = torch.randn(5, 1 << 20, 512, device="cuda", dtype=torch.bfloat16)
+    shapes, starts = np.array([[1024, 1024]]), np.array([0])
+    y, mean, rstd = msda.msda_group_norm(x, shapes, starts, 8)
+    e = x[4].double().view(-1, 8, 64)
+    mu = e.mean((0, 2), keepdim=True)
+    r = 1 / torch.sqrt(((e - mu) ** 2).mean((0, 2), keepdim=True) + 1e-5)
+    want = ((e - mu) * r).view(-1, 512)
+    tol = 2.0 ** -11 * (1 + want.abs()) + 2.0 ** -8 * want.abs()
+    assert bool(((y[4].double() - want).abs() <= tol).all())
+    del e, want, tol
+    gx, _, gb = msda.msda_group_norm_backward(x, shapes, starts, 8, mean, rstd, y)
+    assert bool(torch.isfinite(gx[4]).all()) and bool((gx[4, -1] != x[4, -1]).any())
+    del x, y, gx
+    torch.cuda.empty_cache()
+    # the attention: keys and values as slices of rows of 2^18 values
+    wide = torch.zeros(1, 9000, 1 << 13, 32, device="cuda", dtype=torch.bfloat16)
+    wide[:, :, -4:] = torch.randn(1, 9000, 4, 32, device="cuda").bfloat16()
+    a = dict(q=torch.randn(1, 33, 2, 32, device="cuda").bfloat16(), k=wide[:, :, -2:],
+             v=wide[:, :, -4:-2])
+    out, lse = msda.msda_query_attention(**a)
+    small = {**a, "k": a["k"].contiguous(), "v": a["v"].contiguous()}
+    assert all(torch.equal(s, t) for s, t in zip((out, lse), msda.msda_query_attention(**small)))
+    do = torch.randn(1, 33, 64, device="cuda").bfloat16()
+    assert all(s is None or torch.equal(s, t) for s, t in zip(
+        msda.msda_query_attention_backward(**a, lse=lse, grad_out=do),
+        msda.msda_query_attention_backward(**small, lse=lse, grad_out=do)))
+    attention.check_forward(small, out, lse)
+    del wide, a
+    torch.cuda.empty_cache()
+    # the clipping: one tensor, in place
+    n = (1 << 31) + 12345
+    g = torch.full((n,), 0.5, device="cuda", dtype=torch.bfloat16)
+    total = msda.msda_clip_grad_norm([g], 1.0)
+    want = 0.5 * n ** 0.5
+    assert abs(float(total) - want) <= want * 2.0 ** -23
+    f = torch.tensor(0.5 / (want + 1e-6)).bfloat16()
+    assert bool((g[-20000:] == f.cuda()).all()) and bool((g[:20000] == f.cuda()).all())
+
+
+def test_the_first_call_of_a_process_is_captured():
+    """No call before the capture: nothing that a first call sets up needs a stream."""
+    import subprocess
+    import sys
+    code = """
+import numpy as np, torch
+import scale_deformable_attention_03_b200 as msda
+x = torch.randn(2, 700, 256, device="cuda")
+q = torch.randn(1, 700, 8, 32, device="cuda").bfloat16()
+p, tau = torch.rand(1, 700, 2, device="cuda"), torch.rand(1, 700, 8, device="cuda")
+do = torch.randn(1, 700, 256, device="cuda").bfloat16()
+def step():
+    y, m, r = msda.msda_group_norm(x, np.array([[20, 35]]), np.array([0]), 32)
+    g = msda.msda_group_norm_backward(x, np.array([[20, 35]]), np.array([0]), 32, m, r, y)
+    o, l = msda.msda_query_attention(q, q, q, p, p, tau)
+    h = msda.msda_query_attention_backward(q, q, q, l, do, p, p, tau)
+    n = msda.msda_clip_grad_norm(list(g), 1.0)
+    return [y, m, r, *g, o, l, *h, n]
+s = torch.cuda.Stream()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=s):
+    out = step()
+graph.replay()
+torch.cuda.synchronize()
+first = [t.clone() for t in out]
+assert all(torch.equal(a, b) for a, b in zip(first, step()))
+print("captured first")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
