@@ -281,29 +281,25 @@ struct TileBits {
     uint32_t need[kScan / 32], clear[kScan / 32];
 };
 
-template <bool kOwnKeys, int kScanThreads = kAttnThreads, int kRows = kTile>
+template <bool kOwnKeys>
 __device__ void scan_tiles(TileBits& bits, const GroupRange& own, bool own_full,
                            const int32_t* other, int64_t at, int n, int first, int last)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int w = threadIdx.x; w < kScan / 32; w += kScanThreads) bits.need[w] = bits.clear[w] = 0;
+    for (int w = threadIdx.x; w < kScan / 32; w += kAttnThreads) bits.need[w] = bits.clear[w] = 0;
     __syncthreads();
     for (int tile = first + warp; tile < min(last, first + kScan);
-         tile += kScanThreads / 32) {
-        const int r0 = tile * kRows, count = min(kRows, n - r0);
-        bool need = true, clear = count == kRows;
-        if (other != nullptr) {
-            const GroupRange g = warp_range(other, at + r0, count);
-            const bool meet = g.any && own.any && g.lo <= own.hi && own.lo <= g.hi;
-            if constexpr (kOwnKeys) {
-                need = meet || (own.zero && g.any);
-                clear = clear && own_full && own.all_zero && g.none_below;
-            } else {
-                need = own.any && (meet || g.zero);
-                clear = clear && g.all_zero;
-            }
-        } else if (kOwnKeys) {
-            clear = clear && own_full;
+         tile += kAttnWarps) {
+        const int r0 = tile * kTile, count = min(kTile, n - r0);
+        const GroupRange g = warp_range(other, at + r0, count);
+        const bool meet = g.any && own.any && g.lo <= own.hi && own.lo <= g.hi;
+        bool need, clear = count == kTile;
+        if constexpr (kOwnKeys) {
+            need = meet || (own.zero && g.any);
+            clear = clear && own_full && own.all_zero && g.none_below;
+        } else {
+            need = own.any && (meet || g.zero);
+            clear = clear && g.all_zero;
         }
         if (lane == 0) {
             const int i = tile - first;
