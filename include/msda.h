@@ -1,6 +1,8 @@
 /*
  * msda.h - C ABI of libmsda.so: multi-scale deformable attention (MSDA) and
- * BEVFormer Spatial Cross-Attention (SCA) on NVIDIA B200 (sm_100a).
+ * BEVFormer Spatial Cross-Attention (SCA) on NVIDIA B200 (sm_100a), and the
+ * operators a training step takes beside them: the group norm that makes the
+ * value rows, the attention among object queries, gradient clipping.
  *
  * Sources of the operations (pages this library was written from):
  *   [BQ]  "BEV(三) BEVFormer: how the Query interacts with the 8 Heads of the
@@ -36,11 +38,14 @@
  *     happen while the kernels run surface at the caller's next
  *     synchronisation.  Nothing is launched when the arguments are rejected.
  *     Some kernels are programmatic dependent launches (the SCA compaction's
- *     second pass, the rebatched gather, the camera average): they may begin
+ *     second pass, the rebatched gather, the camera average, the second passes
+ *     of the group norm and of the clipping): they may begin
  *     while the kernel before them in the stream finishes, and wait for it
  *     before they read what it may write or write anything, so stream order
  *     holds as usual, and the calls can be captured into CUDA graphs.
  *   - Outputs are fully overwritten (including gradients and padded rows).
+ *     Outputs and workspace overlap neither inputs nor one another, but where
+ *     a call says so.
  *   - Value rows: pixel (y, x) of level l is row level_start_index[l] +
  *     y * W_l + x; a row holds H heads of MSDA_HEAD_DIM channels.
  *     spatial_shapes[2*l] = H_l (rows), spatial_shapes[2*l+1] = W_l.

@@ -26,7 +26,11 @@
 // with its barrier in between.
 //
 // Bound by memory: the rows are read twice, the second time from L2 as far as
-// that reaches, and written once.
+// that reaches, and written once.  Six cameras (185 k rows of 256, fp32 to bf16):
+// 83 us, 473 MB at 5.7 TB/s with next to nothing left in L2 for the second pass;
+// taking the cameras in twos, so that a pass fits, costs as much in the ends of
+// its launches as it saves.  The gradient of the same in fp32: 162 us, 946 MB at
+// 5.8 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

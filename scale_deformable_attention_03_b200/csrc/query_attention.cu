@@ -11,7 +11,10 @@
 //
 // With 32 channels per head the products are not what binds: a score costs 64
 // multiply-adds, but also an exponential, and a square root per pair of points
-// and two heads, at 16 per clock and SM.
+// and two heads, at 16 per clock and SM.  On the 100 x 100 grid with 8 heads (8e8
+// pairs, 585 us) the exponential unit is busy half of the time, shared memory and
+// instruction issue as well, the matrix pipe a third of it: no one unit binds,
+// four warps per scheduler do not cover one another's latencies.
 #include <algorithm>
 
 #include "query_attention.cuh"
@@ -20,7 +23,7 @@ namespace msda {
 namespace attn {
 namespace {
 
-constexpr int kBlocks = 4;  // CTAs per SM: 128 registers a thread (573 us for the 100 x 100 grid, 603 us with 3)
+constexpr int kBlocks = 4;  // CTAs per SM: 128 registers a thread (5 % faster than three)
 constexpr int kStages = 3;  // tiles in shared memory
 constexpr int kPart = 32;   // keys per step: scores and distances in registers
 

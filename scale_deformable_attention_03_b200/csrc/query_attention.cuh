@@ -6,8 +6,16 @@
 // shared memory.  With 32 channels per head a score takes 32 multiply-adds in
 // each product but also an exponential (16 per clock and SM) and, with the
 // bias, a square root and about ten instructions: the matrix pipe is not what
-// binds, and the fragments of mma.sync leave every score in the thread that
-// computes on it.  A square root serves all heads of a warp.
+// binds (a third busy), and the fragments of mma.sync leave every score in the
+// thread that computes on it.  A square root serves all heads of a warp.
+//
+// The same forward on tcgen05.mma (128 queries per CTA, scores, weights and
+// outputs in tensor memory, one row per thread, one thread issuing) measured
+// slower at this width: 970 us with tiles of 64 keys and two CTAs per SM, 801 us
+// with tiles of 32 and three, where this one took 684 us at that time (100 x 100
+// grid, 8 heads), and twice as long for 900 queries.  Its products have 32 or 64
+// columns, too few to pay for the hand-over of each tile between the issuing
+// thread and the warps that form the weights.
 #pragma once
 
 #include <cuda_bf16.h>
