@@ -580,7 +580,7 @@ typedef enum {
  *   mean, rstd  [B, L, G]    fp32, written; for the backward (NULL: not wanted)
  * The statistics are accumulated relative to values of the data and merged in
  * double (no cancellation when the mean is far from zero), and the same on
- * every run.  eps: finite, > 0.  x, y, gamma and beta 16-byte aligned;
+ * every run; values of a channel differ by less than 1e16 (fp32 squares).  eps: finite, > 0.  x, y, gamma and beta 16-byte aligned;
  * workspace >= msda_group_norm_workspace_size(d) bytes, 256-byte aligned,
  * contents ignored. */
 size_t msda_group_norm_workspace_size(msda_norm_dims_t d);
@@ -644,9 +644,10 @@ typedef struct {
  *     with a negative group are padding, which neither sees nor is seen
  *   lse_i = log sum over seen j of exp(s_ij),
  *   out_i = sum over seen j of exp(s_ij - lse_i) v_j
- * A query that sees nothing gets out = 0 and lse = -infinity.  What rows of
- * padding hold, NaN included, reaches no other row; a key that is seen by some
- * query has to be finite.  Without points there is no bias, without groups
+ * A query that sees nothing gets out = 0 and lse = -infinity.  What padding,
+ * keys that no query sees and queries that see no key hold, NaN included,
+ * reaches no other row.  All other rows have to be finite: a NaN or infinity in
+ * one of them may reach rows that do not see it.  Without points there is no bias, without groups
  * everybody sees everything.
  *   out [B, Nq, H * 32] bf16, written
  *   lse [B, H, Nq]      fp32, written; for the backward (NULL: not wanted)
@@ -696,7 +697,7 @@ typedef struct {
  * summed in double in a fixed order: no overflow, no underflow, the same bits
  * on every run.  A NaN among the gradients makes total and every out NaN; an
  * infinity makes total infinite and f = 0 (so infinite values become NaN).
- * max_norm = +infinity only scales (f = grad_scale).
+ * max_norm = +infinity only scales (f = grad_scale, whatever the gradients hold).
  *   tensors    [count] HOST array, read during the call, not kept
  *   total_norm [1] fp32 device, written
  *   workspace  >= msda_clip_grad_norm_workspace_size(count) bytes, 256-byte

@@ -767,9 +767,11 @@ def sca_backward_inputs(spatial_shapes, level_start_index, attention_logits, pos
 def _same_dense_layout(a, b):
     """Whether a and b hold one value per element in the same order, without gaps."""
     torch = _torch()
-    return a.stride() == b.stride() and (
-        a.is_contiguous() or (a.dim() == 4 and a.is_contiguous(memory_format=torch.channels_last))
-        or (a.dim() == 5 and a.is_contiguous(memory_format=torch.channels_last_3d)))
+    formats = [torch.contiguous_format] + {4: [torch.channels_last],
+                                           5: [torch.channels_last_3d]}.get(a.dim(), [])
+    # (not by the strides: those of dimensions of size 1 say nothing)
+    return any(a.is_contiguous(memory_format=f) and b.is_contiguous(memory_format=f)
+               for f in formats)
 
 
 def msda_clip_grad_norm(grads, max_norm, eps=1e-6, grad_scale=1.0, out=None, total_norm=None,

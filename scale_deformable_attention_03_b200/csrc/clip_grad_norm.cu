@@ -226,10 +226,11 @@ __device__ __forceinline__ void tile_scale(const ClipEntry& e, int64_t k, float 
     }
 }
 
+// (no __restrict__ on what the pass before writes while this one has begun)
 template <int N>
 __global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(
-    const __grid_constant__ ClipTable<N> t, const double* __restrict__ partial, int partials,
-    float max_norm, float eps, float scale, float* __restrict__ total_norm)
+    const __grid_constant__ ClipTable<N> t, const double* partial, int partials, float max_norm,
+    float eps, float scale, float* total_norm)
 {
     __shared__ double warp_sum[kClipThreads / 32];
     __shared__ float factor;

@@ -636,10 +636,11 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_stats_kernel(const void*
     norm_stats<kX>(sm, x, n, part, middle);
 }
 
+// (no __restrict__ on what the first pass writes while this one has begun)
 template <bool kX, bool kY, int kAct>
 __global__ void __launch_bounds__(kNormThreads, 2) norm_apply_kernel(
-    const void* __restrict__ x, const NormShape n, const double2* __restrict__ part,
-    const double* __restrict__ middle, const NormOut out)
+    const void* __restrict__ x, const NormShape n, const double2* part, const double* middle,
+    const NormOut out)
 {
     __shared__ ApplySmem sm;
     norm_apply<kX, kY, kAct>(sm, x, n, part, middle, out, n.runs - 1 - (int)blockIdx.x,
@@ -904,8 +905,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_grad_sums_kernel(
 // The CTAs behind the runs take a block of the parameters' gradients each.
 template <bool kX, bool kDy, bool kDx, int kAct>
 __global__ void __launch_bounds__(kNormThreads, 2) norm_grad_apply_kernel(
-    const GradIn in, const NormShape n, const float* __restrict__ chan,
-    const double2* __restrict__ part, const GradOut out)
+    const GradIn in, const NormShape n, const float* chan, const double2* part, const GradOut out)
 {
     __shared__ GradSmem sm;
     const int i = (int)blockIdx.x - n.runs;

@@ -12,7 +12,7 @@
 // With 32 channels per head the products are not what binds: a score costs 64
 // multiply-adds, but also an exponential, and a square root per pair of points
 // and two heads, at 16 per clock and SM.  On the 100 x 100 grid with 8 heads (8e8
-// pairs, 585 us) the exponential unit is busy half of the time, shared memory and
+// pairs, 580 us) the exponential unit is busy half of the time, shared memory and
 // instruction issue as well, the matrix pipe a third of it: no one unit binds,
 // four warps per scheduler do not cover one another's latencies.
 #include <algorithm>
@@ -36,7 +36,7 @@ struct ForwardArgs {
 
 // Tiles that a CTA keeps where splits only even out the last wave (18 tiles in
 // three parts: 37 us for the first pass of the gradient of 1100 queries, 29 us
-// in one; 79 tiles in two: 166 us for 5000 queries, 181 us in one).
+// in one; 79 tiles in two: 155 us for 5000 queries, 181 us in one).
 constexpr int kEvenTiles = 32;
 constexpr int kPartRow = 36;  // floats of a row of split sums, padded for the banks
 
@@ -49,20 +49,19 @@ struct ForwardSmem {
     TileBits bits;
 };
 
-template <int HP, bool kBias>
+template <int HP, bool kBias, bool kGroups>
 __device__ __forceinline__ void load_keys(ForwardSmem<HP>& sm, int stage, const Inputs& in,
-                                          const TileCopy<HP>& copy, int b, int tile)
+                                          const TileCopy<HP>& copy,
+                                          const Tiles<kGroups>& set, int b, int tile)
 {
-    const int64_t first = (int64_t)b * in.Nk;
-    // what padding rows hold must not meet a weight of zero
-    const bool all = in.kg == nullptr && tile * kTile + kTile <= in.Nk;
-    copy.fetch(smem_addr(sm.k[stage]), smem_addr(sm.v[stage]), tile, all,
-               [&](int key) { return in.kg == nullptr || __ldg(in.kg + first + key) >= 0; });
-    load_columns<kBias>(sm.pos[stage], sm.group[stage], in.kp, in.kg, first, tile * kTile, in.Nk);
+    copy.fetch(smem_addr(sm.k[stage]), smem_addr(sm.v[stage]), tile, set.clear(tile),
+               set.rows(tile));
+    load_columns<kBias, kGroups>(sm.pos[stage], sm.group[stage], in.kp, in.kg,
+                                 (int64_t)b * in.Nk, tile * kTile, in.Nk);
     cp_commit();
 }
 
-template <int HP, bool kBias>
+template <int HP, bool kBias, bool kGroups>
 __global__ void __launch_bounds__(kAttnThreads, kBlocks)
     attention_forward_kernel(const ForwardArgs a)
 {
@@ -103,11 +102,9 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocks)
         }
     }
     int g0 = 0, g1 = 0;
-    GroupRange own{0, 0, true, true, true, true};
-    if (in.qg != nullptr) {
+    if constexpr (kGroups) {
         g0 = on0 ? __ldg(in.qg + q0) : -1;
         g1 = on1 ? __ldg(in.qg + q0 + 8) : -1;
-        own = warp_range(in.qg, (int64_t)b * in.Nq + qt * kRows, min(kRows, in.Nq - qt * kRows));
     }
     // The reference that is taken off stays the same until a score is 2^kSlack
     // times above it: weights up to 2^kSlack are as exact as weights up to 1, and
@@ -125,20 +122,21 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocks)
     const int tiles = (in.Nk + kTile - 1) / kTile;
     const int begin = split * a.split_tiles, last = min(tiles, begin + a.split_tiles);
     for (int first = begin; first < last;) {
-        const Tiles set{sm.bits, in.kg != nullptr, first, last, in.Nk / kTile};
+        const Tiles<kGroups> set{sm.bits, first, last, in.Nk / kTile};
         first = set.end();
-        if (set.grouped) {
+        if constexpr (kGroups) {
             __syncthreads();  // the bits of the tiles before are read
-            scan_tiles<false>(sm.bits, own, true, in.kg, (int64_t)b * in.Nk, in.Nk, set.first,
-                              last);
+            scan_tiles<false>(sm.bits, in.qg + (int64_t)b * in.Nq + qt * kRows,
+                              min(kRows, in.Nq - qt * kRows), in.kg + (int64_t)b * in.Nk, in.Nk,
+                              set.first, last);
         }
         int tile = set.next(set.first), stage = 0;
         if (tile >= last) continue;
-        load_keys<HP, kBias>(sm, 0, in, copy, b, tile);
+        load_keys<HP, kBias, kGroups>(sm, 0, in, copy, set, b, tile);
         cp_wait<0>();
         __syncthreads();
         int ahead = set.next(tile + 1);
-        if (ahead < last) load_keys<HP, kBias>(sm, 1, in, copy, b, ahead);
+        if (ahead < last) load_keys<HP, kBias, kGroups>(sm, 1, in, copy, set, b, ahead);
 
         // A step is 32 keys of a head.  Its products are asked for one step early,
         // so that the matrix pipe works while the weights of the step before are
@@ -183,7 +181,7 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocks)
                     const int at = kPart * part + 8 * j + 2 * t;
                     const int key = of_tile * kTile + at;
                     int2 kg = make_int2(0, 0);
-                    if (in.kg != nullptr) kg = *reinterpret_cast<const int2*>(&sm.group[st][at]);
+                    if constexpr (kGroups) kg = *reinterpret_cast<const int2*>(&sm.group[st][at]);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int qg = half ? g1 : g0;
@@ -234,8 +232,8 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocks)
                     cp_wait<0>();     // the next tile is here, and
                     __syncthreads();  // nobody reads the one before this any more
                     if (after < last)
-                        load_keys<HP, kBias>(sm, next == kStages - 1 ? 0 : next + 1, in, copy, b,
-                                             after);
+                        load_keys<HP, kBias, kGroups>(sm, next == kStages - 1 ? 0 : next + 1, in, copy,
+                                                      set, b, after);
                     products(next, 0, 0);  // (of no use behind the last tile)
                 } else {
                     products(stage, (u + 1) / HP, (u + 1) % HP);
@@ -348,14 +346,15 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocks)
     cluster_sync();  // nobody's shared memory goes while others read it
 }
 
-template <int HP, bool kBias>
+template <int HP, bool kBias, bool kGroups>
 cudaError_t run(const ForwardArgs& a, cudaStream_t s)
 {
-    const cudaError_t e = allow_shared<attention_forward_kernel<HP, kBias>>(sizeof(ForwardSmem<HP>));
+    constexpr auto kernel = attention_forward_kernel<HP, kBias, kGroups>;
+    const cudaError_t e = allow_shared<kernel>(sizeof(ForwardSmem<HP>));
     if (e != cudaSuccess) return e;
     const int64_t ctas = (int64_t)a.q_tiles * a.in.B * (a.in.H / HP) * a.splits;
-    return launch_clusters(attention_forward_kernel<HP, kBias>, a.splits, dim3((unsigned)ctas),
-                           dim3(kAttnThreads), sizeof(ForwardSmem<HP>), s, a);
+    return launch_clusters(kernel, a.splits, dim3((unsigned)ctas), dim3(kAttnThreads),
+                           sizeof(ForwardSmem<HP>), s, a);
 }
 
 }  // namespace
@@ -509,8 +508,9 @@ extern "C" msda_status_t msda_query_attention(const msda_attention_t* p, void* o
     a.splits = plan.splits;
     a.split_tiles = plan.split_tiles;
     const cudaStream_t s = (cudaStream_t)stream;
-    return api_cuda(plan.heads == 2 ? run<2, true>(a, s)
-                    : p->tau        ? run<1, true>(a, s)
-                                    : run<1, false>(a, s),
-                    "msda_query_attention");
+    const bool groups = p->q_group || p->k_group;
+    const auto call = plan.heads == 2 ? (groups ? run<2, true, true> : run<2, true, false>)
+                      : p->tau        ? (groups ? run<1, true, true> : run<1, true, false>)
+                                      : (groups ? run<1, false, true> : run<1, false, false>);
+    return api_cuda(call(a, s), "msda_query_attention");
 }

@@ -35,7 +35,10 @@ constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kRows = 16 * kAttnWarps;  // rows of the own side per CTA
 constexpr int kTile = 64;           // rows of the other side per step
 constexpr int kDim = 32;
-constexpr int kScan = 2048;         // tiles whose visibility is looked up at once
+constexpr int kScan = 256;          // tiles whose visibility is looked up at once
+// Groups that a bit each tells apart (10 000 queries in 100 groups, mixed: 955 us
+// forward with bits, 991 us with the groups sorted, 1268 us looked through).
+constexpr int kGroupBits = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -209,9 +212,10 @@ struct TileCopy {
         to = (c / 4) * kTileBytes + tile_at(row, c % 4);
     }
 
-    // on(row): whether the row holds something; others are filled with zeros.
-    template <typename F>
-    __device__ __forceinline__ void fetch(uint32_t sa, uint32_t sb, int tile, bool all, F on) const
+    // `all` the tile's rows, or those of the item whose bit is set in `keep`, the
+    // others as zeros.
+    __device__ __forceinline__ void fetch(uint32_t sa, uint32_t sb, int tile, bool all,
+                                          uint2 keep) const
     {
         const int64_t r0 = (int64_t)tile * kTile;
         const char *pa = a + r0 * lda, *pb = b + r0 * ldb;
@@ -231,7 +235,8 @@ struct TileCopy {
 #pragma unroll 1
         for (int i = 0; i < kTile / kStep; ++i) {
             const int r = tile * kTile + row + i * kStep;
-            const bool there = r < n && on(r);
+            const int at = row + i * kStep;
+            const bool there = r < n && ((at < 32 ? keep.x : keep.y) >> (at & 31) & 1);
             cp_async<16>(ta + i * kStep * 64, there ? pa : a - row * lda, there);
             cp_async<16>(tb + i * kStep * 64, there ? pb : b - row * ldb, there);
             pa += kStep * lda;
@@ -256,62 +261,103 @@ __device__ __forceinline__ void load_rows(uint32_t (&f)[8], const __nv_bfloat16*
     }
 }
 
-// The groups on one side, as far as visibility goes; lo and hi: of those >= 0.
+// The groups of the own side's rows; lo and hi: of those >= 0.
 struct GroupRange {
     int lo, hi;
-    bool any, zero, all_zero, none_below;  // some >= 0, some 0, all 0, none negative
+    bool zero, all_zero;  // some 0, all 0
 };
 
-__device__ __forceinline__ GroupRange warp_range(const int32_t* g, int64_t at, int count)
+__device__ __forceinline__ GroupRange warp_range(const int32_t* g, int count)
 {
     int lo = INT32_MAX, hi = -1;
-    bool zero = false, all = true, below = false;
+    bool zero = false, all = true;
     for (int i = threadIdx.x & 31; i < count; i += 32) {
-        const int v = __ldg(g + at + i);
+        const int v = __ldg(g + i);
         if (v >= 0) {
             lo = min(lo, v);
             hi = max(hi, v);
         }
         zero |= v == 0;
         all &= v == 0;
-        below |= v < 0;
     }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    return {lo, hi, hi >= 0, (bool)__any_sync(0xffffffffu, zero),
-            (bool)__all_sync(0xffffffffu, all), !__any_sync(0xffffffffu, below)};
+    return {__reduce_min_sync(0xffffffffu, lo), __reduce_max_sync(0xffffffffu, hi),
+            (bool)__any_sync(0xffffffffu, zero), (bool)__all_sync(0xffffffffu, all)};
 }
 
-// Tiles of the other side that some row of the own side needs (bit set in
-// `need`), and those in which no pair is masked (`clear`), for kScan tiles
-// from `first` on.  kOwnKeys: the own side are keys and the other queries.
+// What is looked up for kScan tiles of the other side at once: its rows that see
+// or are seen by some row of the own side (`rows`; the others are not read, so
+// that a weight of zero never meets what they hold), the tiles that have such a
+// row (bit set in `need`), and those in which no pair is masked (`clear`).
 struct TileBits {
+    uint2 rows[kScan];
     uint32_t need[kScan / 32], clear[kScan / 32];
+    // the own side's groups: a bit each, modulo kGroupBits, where they lie that close
+    // together, else sorted
+    union {
+        uint32_t own[kGroupBits / 32];
+        int32_t sorted[kRows];
+    };
 };
 
+// kOwnKeys: the own side (`count` rows from `mine` on) are keys and the other
+// (`n` rows from `other` on) queries.
 template <bool kOwnKeys>
-__device__ void scan_tiles(TileBits& bits, const GroupRange& own, bool own_full,
-                           const int32_t* other, int64_t at, int n, int first, int last)
+__device__ void scan_tiles(TileBits& bits, const int32_t* mine, int count, const int32_t* other,
+                           int n, int first, int last)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const GroupRange own = warp_range(mine, count);
     for (int w = threadIdx.x; w < kScan / 32; w += kAttnThreads) bits.need[w] = bits.clear[w] = 0;
-    __syncthreads();
-    for (int tile = first + warp; tile < min(last, first + kScan);
-         tile += kAttnWarps) {
-        const int r0 = tile * kTile, count = min(kTile, n - r0);
-        const GroupRange g = warp_range(other, at + r0, count);
-        const bool meet = g.any && own.any && g.lo <= own.hi && own.lo <= g.hi;
-        bool need, clear = count == kTile;
-        if constexpr (kOwnKeys) {
-            need = meet || (own.zero && g.any);
-            clear = clear && own_full && own.all_zero && g.none_below;
-        } else {
-            need = own.any && (meet || g.zero);
-            clear = clear && g.all_zero;
+    const bool wide = own.hi >= 0 && own.hi - own.lo >= kGroupBits;
+    const int mine_here = (int)threadIdx.x < count ? __ldg(mine + threadIdx.x) : -1;
+    if (!wide) {
+        for (int w = threadIdx.x; w < kGroupBits / 32; w += kAttnThreads) bits.own[w] = 0;
+        __syncthreads();
+        if (mine_here >= 0)
+            atomicOr(&bits.own[mine_here / 32 % (kGroupBits / 32)], 1u << (mine_here & 31));
+    } else if ((int)threadIdx.x < count) {
+        int rank = 0;
+        for (int i = 0; i < count; ++i) {
+            const int v = __ldg(mine + i);
+            rank += v < mine_here || (v == mine_here && i < (int)threadIdx.x);
         }
+        bits.sorted[rank] = mine_here;
+    }
+    __syncthreads();
+    const auto has = [&](int v) {  // whether the own side has this group
+        if (v < own.lo || v > own.hi) return false;
+        if (!wide) return (bool)(bits.own[v / 32 % (kGroupBits / 32)] >> (v & 31) & 1);
+        int lo = 0, hi = count - 1;  // the last one is own.hi, so one at least is >= v
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (bits.sorted[mid] < v) lo = mid + 1;
+            else hi = mid;
+        }
+        return bits.sorted[lo] == v;
+    };
+    for (int tile = first + warp; tile < min(last, first + kScan); tile += kAttnWarps) {
+        uint32_t meet[2];
+        bool clear = true;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int row = tile * kTile + 32 * half + lane;
+            const int v = row < n ? __ldg(other + row) : -1;
+            bool seen = v >= 0 && own.hi >= 0;
+            if constexpr (kOwnKeys) {
+                seen = seen && (own.zero || has(v));
+                clear = clear && v >= 0;
+            } else {
+                seen = seen && (v == 0 || has(v));
+                clear = clear && v == 0;
+            }
+            meet[half] = __ballot_sync(0xffffffffu, seen);
+        }
+        if constexpr (kOwnKeys) clear = clear && count == kTile && own.all_zero;
+        clear = __all_sync(0xffffffffu, clear);
         if (lane == 0) {
             const int i = tile - first;
-            if (need) atomicOr(&bits.need[i >> 5], 1u << (i & 31));
+            bits.rows[i] = make_uint2(meet[0], meet[1]);
+            if (meet[0] | meet[1]) atomicOr(&bits.need[i >> 5], 1u << (i & 31));
             if (clear) atomicOr(&bits.clear[i >> 5], 1u << (i & 31));
         }
     }
@@ -336,23 +382,28 @@ __device__ __forceinline__ int next_tile(const TileBits& bits, int tile, int fir
 
 // The tiles from `first` on, up to `last`: all of them without groups, those
 // that have been looked up with.
+template <bool kGroups>
 struct Tiles {
     const TileBits& bits;
-    bool grouped;
     int first, last;
     int full;  // without groups: tiles below it have no pair masked
 
     __device__ __forceinline__ int next(int tile) const
     {
-        return grouped ? next_tile(bits, tile, first, last) : min(tile, last);
+        return kGroups ? next_tile(bits, tile, first, last) : min(tile, last);
     }
     __device__ __forceinline__ bool clear(int tile) const
     {
         const int i = tile - first;
-        return grouped ? (bits.clear[i >> 5] >> (i & 31)) & 1 : tile < full;
+        return kGroups ? (bits.clear[i >> 5] >> (i & 31)) & 1 : tile < full;
+    }
+    // The rows of a tile that are read; `clear` tiles are read as a whole.
+    __device__ __forceinline__ uint2 rows(int tile) const
+    {
+        return kGroups ? bits.rows[tile - first] : make_uint2(~0u, ~0u);
     }
     // Where the tiles after these start.
-    __device__ __forceinline__ int end() const { return grouped ? first + kScan : last; }
+    __device__ __forceinline__ int end() const { return kGroups ? first + kScan : last; }
 };
 
 __device__ __forceinline__ bool sees(int q_group, int k_group)
@@ -374,7 +425,7 @@ struct Points {
 };
 
 // The points and groups of the tile's rows r0 .. r0 + 63 of an item.
-template <bool kBias>
+template <bool kBias, bool kGroups>
 __device__ __forceinline__ void load_columns(Points& pos, int32_t* group, const float2* points,
                                              const int32_t* groups, int64_t first, int r0, int n)
 {
@@ -386,7 +437,7 @@ __device__ __forceinline__ void load_columns(Points& pos, int32_t* group, const 
         cp_async<4>(smem_addr(&pos.x[threadIdx.x]), &src->x, on);
         cp_async<4>(smem_addr(&pos.y[threadIdx.x]), &src->y, on);
     }
-    if (groups != nullptr)
+    if constexpr (kGroups)
         cp_async<4>(smem_addr(group + threadIdx.x), on ? groups + first + row : groups, on);
 }
 
@@ -434,7 +485,7 @@ constexpr int kSms = 148;
 // and shorter CTAs are faster).  The keys are split until the CTAs fill a wave,
 // down to two tiles per CTA, and of long rows where it evens out the last wave:
 // 628 CTAs in waves of 592 take two of them (704 us for the 100 x 100 grid),
-// quartered they take five a quarter as long (585 us).
+// quartered they take five a quarter as long (580 us).
 struct Plan {
     int heads, splits, split_tiles;
 };

@@ -10,8 +10,8 @@
 // (not from the rounded output of the forward): ds is then exact where one key
 // takes all the weight, and dtau, an fp32 sum of it, keeps fp32's precision.
 //
-// Like the forward it is bound by no single unit (5000 queries, 8 heads: 167 us for
-// D, exponential unit 60 % busy; 425 us for the gradients, shared memory 58 %,
+// Like the forward it is bound by no single unit (5000 queries, 8 heads: 155 us for
+// D, exponential unit 60 % busy; 403 us for the gradients, shared memory 58 %,
 // issue 48 %, exponentials 43 %, matrix pipe 37 %): an exponential and a square
 // root per pair in each of the three walks, and nine products for the five that a
 // single walk with atomics would take.
@@ -47,33 +47,27 @@ struct BackwardSmem {
     TileBits bits;
 };
 
-template <int HP, bool kBias>
+template <int HP, bool kBias, bool kGroups>
 __device__ __forceinline__ void load_keys(BackwardSmem<HP>& sm, int stage, const Inputs& in,
-                                          const TileCopy<HP>& copy, int b, int tile)
+                                          const TileCopy<HP>& copy,
+                                          const Tiles<kGroups>& set, int b, int tile)
 {
-    const int64_t first = (int64_t)b * in.Nk;
-    const bool all = in.kg == nullptr && tile * kTile + kTile <= in.Nk;
-    copy.fetch(smem_addr(sm.a[stage]), smem_addr(sm.b[stage]), tile, all,
-               [&](int key) { return in.kg == nullptr || __ldg(in.kg + first + key) >= 0; });
-    load_columns<kBias>(sm.pos[stage], sm.group[stage], in.kp, in.kg, first, tile * kTile, in.Nk);
+    copy.fetch(smem_addr(sm.a[stage]), smem_addr(sm.b[stage]), tile, set.clear(tile),
+               set.rows(tile));
+    load_columns<kBias, kGroups>(sm.pos[stage], sm.group[stage], in.kp, in.kg,
+                                 (int64_t)b * in.Nk, tile * kTile, in.Nk);
     cp_commit();
 }
 
-// With groups, queries that see nothing (lse = -infinity) read as zero: whatever
-// they and their gradient hold, p = 0 then has nothing to meet.  (Without groups
-// there is no padding, and no tile waits for its lse: 421 us instead of 453 us
-// for the second kernel on 5000 queries.)
-template <int HP, bool kBias>
+template <int HP, bool kBias, bool kGroups>
 __device__ __forceinline__ void load_queries(BackwardSmem<HP>& sm, int stage,
                                              const BackwardArgs& a, const TileCopy<HP>& copy,
-                                             int b, int h, int tile)
+                                             const Tiles<kGroups>& set, int b, int h, int tile)
 {
     const Inputs& in = a.in;
     const int r0 = tile * kTile;
-    const float* lse = a.lse + ((int64_t)b * in.H + h + threadIdx.x % TileCopy<HP>::kChunks / 4) * in.Nq;
-    copy.fetch(smem_addr(sm.a[stage]), smem_addr(sm.b[stage]), tile,
-               in.qg == nullptr && r0 + kTile <= in.Nq,
-               [&](int q) { return in.qg == nullptr || __ldg(lse + q) != -INFINITY; });
+    copy.fetch(smem_addr(sm.a[stage]), smem_addr(sm.b[stage]), tile, set.clear(tile),
+               set.rows(tile));
     const int64_t plane = (int64_t)in.B * in.H * in.Nq;
 #pragma unroll
     for (int i0 = 0; i0 < 3 * HP * kTile; i0 += kAttnThreads) {
@@ -84,7 +78,7 @@ __device__ __forceinline__ void load_queries(BackwardSmem<HP>& sm, int stage,
         const float* src = a.rows + k * plane + ((int64_t)b * in.H + h + hh) * in.Nq + row;
         cp_async<4>(smem_addr(&sm.rows[stage][hh][k][i % kTile]), on ? src : a.rows, on);
     }
-    load_columns<kBias>(sm.pos[stage], sm.group[stage], in.qp, in.qg, (int64_t)b * in.Nq, r0,
+    load_columns<kBias, kGroups>(sm.pos[stage], sm.group[stage], in.qp, in.qg, (int64_t)b * in.Nq, r0,
                         in.Nq);
     cp_commit();
 }
@@ -153,7 +147,7 @@ __device__ __forceinline__ float quad_sum(float x)
 
 // 64 queries and the tiles [begin, last) of the keys: D (and what the last
 // kernel needs of the queries beside it), or with kGrad, given D, dq and dtau.
-template <int HP, bool kBias, bool kGrad>
+template <int HP, bool kBias, bool kGroups, bool kGrad>
 __device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardArgs& a, int id,
                                           int split)
 {
@@ -198,11 +192,9 @@ __device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardAr
         }
     }
     int g0 = 0, g1 = 0;
-    GroupRange own{0, 0, true, true, true, true};
-    if (in.qg != nullptr) {
+    if constexpr (kGroups) {
         g0 = on0 ? __ldg(in.qg + q0) : -1;
         g1 = on1 ? __ldg(in.qg + q0 + 8) : -1;
-        own = warp_range(in.qg, (int64_t)b * in.Nq + qt * kRows, min(kRows, in.Nq - qt * kRows));
     }
     const float scale = in.scale * kLog2e;
     float D[HP][2] = {}, dt[HP][2] = {}, dq[HP][4][4] = {};
@@ -223,19 +215,20 @@ __device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardAr
     const TileCopy<HP> copy(in.k + (int64_t)b * in.Nk * in.ldk + h * kDim, in.ldk,
                             in.v + (int64_t)b * in.Nk * in.ldv + h * kDim, in.ldv, in.Nk);
     for (int first = begin; first < last;) {
-        const Tiles set{sm.bits, in.kg != nullptr, first, last, in.Nk / kTile};
+        const Tiles<kGroups> set{sm.bits, first, last, in.Nk / kTile};
         first = set.end();
-        if (set.grouped) {
+        if constexpr (kGroups) {
             __syncthreads();  // the bits of the tiles before are read
-            scan_tiles<false>(sm.bits, own, true, in.kg, (int64_t)b * in.Nk, in.Nk, set.first,
-                              last);
+            scan_tiles<false>(sm.bits, in.qg + (int64_t)b * in.Nq + qt * kRows,
+                              min(kRows, in.Nq - qt * kRows), in.kg + (int64_t)b * in.Nk, in.Nk,
+                              set.first, last);
         }
         int tile = set.next(set.first), stage = 0;
-        if (tile < last) load_keys<HP, kBias>(sm, stage, in, copy, b, tile);
+        if (tile < last) load_keys<HP, kBias, kGroups>(sm, stage, in, copy, set, b, tile);
         while (tile < last) {
             const int ahead = set.next(tile + 1);
             if (ahead < last) {
-                load_keys<HP, kBias>(sm, stage ^ 1, in, copy, b, ahead);
+                load_keys<HP, kBias, kGroups>(sm, stage ^ 1, in, copy, set, b, ahead);
                 cp_wait<1>();
             } else {
                 cp_wait<0>();
@@ -263,7 +256,7 @@ __device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardAr
                         for (int c = 0; c < 2; ++c) {
                             const int at = kHalf * st + 8 * j + 2 * t + c;
                             const bool in_range = tile * kTile + at < in.Nk;
-                            const int kg = in.kg != nullptr ? sm.group[stage][at] : 0;
+                            const int kg = kGroups ? sm.group[stage][at] : 0;
                             hide |= (uint32_t)!(in_range && sees(g0, kg)) << (4 * j + c);
                             hide |= (uint32_t)!(in_range && sees(g1, kg)) << (4 * j + 2 + c);
                         }
@@ -370,7 +363,7 @@ __device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardAr
 }
 
 // 64 keys and all queries: dk and dv.
-template <int HP, bool kBias>
+template <int HP, bool kBias, bool kGroups>
 __device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const BackwardArgs& a, int id)
 {
     const Inputs& in = a.in;
@@ -382,12 +375,10 @@ __device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const Backwar
     const bool on0 = row < in.Nk, on1 = row + 8 < in.Nk;
     const int64_t k0 = (int64_t)b * in.Nk + row;
     int g0 = on0 ? 0 : -1, g1 = on1 ? 0 : -1;
-    GroupRange own{0, 0, true, true, true, true};
     const int own_rows = min(kRows, in.Nk - kt * kRows);
-    if (in.kg != nullptr) {
+    if constexpr (kGroups) {
         if (on0) g0 = __ldg(in.kg + k0);
         if (on1) g1 = __ldg(in.kg + k0 + 8);
-        own = warp_range(in.kg, (int64_t)b * in.Nk + kt * kRows, own_rows);
     }
     uint32_t kf[HP][8], vf[HP][8];
 #pragma unroll
@@ -415,20 +406,20 @@ __device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const Backwar
                             in.Nq);
     const int tiles = a.q_tiles;
     for (int first = 0; first < tiles;) {
-        const Tiles set{sm.bits, in.qg != nullptr, first, tiles,
-                        own_rows == kRows ? in.Nq / kTile : 0};
+        const Tiles<kGroups> set{sm.bits, first, tiles,
+                                 own_rows == kRows ? in.Nq / kTile : 0};
         first = set.end();
-        if (set.grouped) {
+        if constexpr (kGroups) {
             __syncthreads();
-            scan_tiles<true>(sm.bits, own, own_rows == kRows, in.qg, (int64_t)b * in.Nq, in.Nq,
-                             set.first, tiles);
+            scan_tiles<true>(sm.bits, in.kg + (int64_t)b * in.Nk + kt * kRows, own_rows,
+                             in.qg + (int64_t)b * in.Nq, in.Nq, set.first, tiles);
         }
         int tile = set.next(set.first), stage = 0;
-        if (tile < tiles) load_queries<HP, kBias>(sm, stage, a, copy, b, h, tile);
+        if (tile < tiles) load_queries<HP, kBias, kGroups>(sm, stage, a, copy, set, b, h, tile);
         while (tile < tiles) {
             const int ahead = set.next(tile + 1);
             if (ahead < tiles) {
-                load_queries<HP, kBias>(sm, stage ^ 1, a, copy, b, h, ahead);
+                load_queries<HP, kBias, kGroups>(sm, stage ^ 1, a, copy, set, b, h, ahead);
                 cp_wait<1>();
             } else {
                 cp_wait<0>();
@@ -456,7 +447,7 @@ __device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const Backwar
                         for (int c = 0; c < 2; ++c) {
                             const int at = kHalf * st + 8 * j + 2 * t + c;
                             const bool in_range = tile * kTile + at < in.Nq;
-                            const int qg = in.qg != nullptr ? sm.group[stage][at] : 0;
+                            const int qg = kGroups ? sm.group[stage][at] : 0;
                             hide |= (uint32_t)!(in_range && sees(qg, g0)) << (4 * j + c);
                             hide |= (uint32_t)!(in_range && sees(qg, g1)) << (4 * j + 2 + c);
                         }
@@ -485,6 +476,8 @@ __device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const Backwar
                             dp[j][half] = __fmul2_rn(
                                 s[j][half],
                                 __fadd2_rn(dp[j][half], make_float2(-r[2].x, -r[2].y)));
+                            // (a key that nobody sees may hold anything)
+                            if (!clear) mask(dp[j][half], hide >> (4 * j + 2 * half), 0.0f);
                         }
                     }
                     accumulate(dv[hh], s, so, st, lanes);
@@ -503,38 +496,39 @@ __device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const Backwar
     }
 }
 
-template <int HP, bool kBias>
+template <int HP, bool kBias, bool kGroups>
 __global__ void __launch_bounds__(kAttnThreads, kBlocks) attention_dots_kernel(const BackwardArgs a)
 {
     __shared__ BackwardSmem<HP> sm;
     const int id = blockIdx.x / a.splits;
-    walk_keys<HP, kBias, false>(sm, a, id, blockIdx.x - id * a.splits);
+    walk_keys<HP, kBias, kGroups, false>(sm, a, id, blockIdx.x - id * a.splits);
 }
 
-template <bool kBias>
+template <bool kBias, bool kGroups>
 __global__ void __launch_bounds__(kAttnThreads, kBlocks) attention_grad_kernel(const BackwardArgs a)
 {
     __shared__ BackwardSmem<1> sm;
     const int keys = a.k_tiles * a.in.H * a.in.B;  // the longer ones first
-    if ((int)blockIdx.x < keys) walk_queries<1, kBias>(sm, a, blockIdx.x);
-    else walk_keys<1, kBias, true>(sm, a, blockIdx.x - keys, 0);
+    if ((int)blockIdx.x < keys) walk_queries<1, kBias, kGroups>(sm, a, blockIdx.x);
+    else walk_keys<1, kBias, kGroups, true>(sm, a, blockIdx.x - keys, 0);
 }
 
+template <bool kGroups>
 cudaError_t run(const BackwardArgs& a, const Plan& plan, bool bias, cudaStream_t s)
 {
     const int64_t items = (int64_t)a.in.B * a.in.H;
     cudaError_t e = cudaSuccess;
     if (a.in.Nq > 0) {
         const unsigned ctas = (unsigned)(items / plan.heads * a.q_tiles * a.splits);
-        const auto kernel = plan.heads == 2 ? attention_dots_kernel<2, true>
-                            : bias          ? attention_dots_kernel<1, true>
-                                            : attention_dots_kernel<1, false>;
+        const auto kernel = plan.heads == 2 ? attention_dots_kernel<2, true, kGroups>
+                            : bias          ? attention_dots_kernel<1, true, kGroups>
+                                            : attention_dots_kernel<1, false, kGroups>;
         e = launch_clusters(kernel, a.splits, dim3(ctas), dim3(kAttnThreads), 0, s, a);
         if (e != cudaSuccess) return e;
     }
     const unsigned ctas = (unsigned)(items * (a.q_tiles + a.k_tiles));
-    if (bias) attention_grad_kernel<true><<<ctas, kAttnThreads, 0, s>>>(a);
-    else attention_grad_kernel<false><<<ctas, kAttnThreads, 0, s>>>(a);
+    if (bias) attention_grad_kernel<true, kGroups><<<ctas, kAttnThreads, 0, s>>>(a);
+    else attention_grad_kernel<false, kGroups><<<ctas, kAttnThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -571,6 +565,7 @@ extern "C" msda_status_t msda_query_attention_backward(const msda_attention_t* p
             return bad("grad_q is null or not 16-byte aligned");
         if (p->tau != nullptr && (grad_tau == nullptr || (uintptr_t)grad_tau % 4))
             return bad("grad_tau is null or not 4-byte aligned");
+        if (p->tau == nullptr && grad_tau != nullptr) return bad("grad_tau without tau");
     }
     if (p->Nk > 0 && (grad_k == nullptr || grad_v == nullptr || (uintptr_t)grad_k % 16 ||
                       (uintptr_t)grad_v % 16))
@@ -597,6 +592,8 @@ extern "C" msda_status_t msda_query_attention_backward(const msda_attention_t* p
     a.q_tiles = (p->Nq + kTile - 1) / kTile;
     a.k_tiles = (p->Nk + kTile - 1) / kTile;
     const cudaStream_t s = (cudaStream_t)stream;
-    const cudaError_t e = run(a, plan, p->tau != nullptr, s);
+    const bool bias = p->tau != nullptr;
+    const cudaError_t e = p->q_group || p->k_group ? run<true>(a, plan, bias, s)
+                                                   : run<false>(a, plan, bias, s);
     return api_cuda(e, "msda_query_attention_backward");
 }

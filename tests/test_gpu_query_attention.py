@@ -204,6 +204,38 @@ def test_documents_are_independent():
         at += m
 
 
+@pytest.mark.parametrize("step", [1, 10, 1000, 64_000_000])
+@pytest.mark.parametrize("bias", [False, True])
+def test_what_nobody_sees_reaches_nothing(bias, step):
+    """Keys of groups that no query has and queries of groups that no key has hold NaN; the
+    groups lie close together, far apart and 64 apart modulo the others."""
+    B, Nq, Nk, H = 2, 150, 260, 2
+    a = problem(B, Nq, Nk, H, bias, None, 21, joint=False)
+    g = torch.Generator(device="cuda").manual_seed(22)
+    qg = 1 + step * torch.randint(0, 24, (B, Nq), generator=g, device="cuda", dtype=torch.int32)
+    kg = 1 + step * torch.randint(0, 32, (B, Nk), generator=g, device="cuda", dtype=torch.int32)
+    qg[qg == 1 + 5 * step] = 1 + 6 * step   # a hole within the queries' groups,
+    qg[qg == 1 + 7 * step] = 1
+    kg[kg == 1 + 9 * step] = 1              # and one within the keys'
+    a.update(q_group=qg, k_group=kg)
+    sees = qg[:, :, None] == kg[:, None]
+    q_off, k_off = ~sees.any(2), ~sees.any(1)
+    assert bool(q_off.any()) and bool(k_off.any())
+    a["q"][q_off], a["k"][k_off], a["v"][k_off] = float("nan"), float("nan"), float("inf")
+    if bias:
+        a["q_points"][q_off], a["k_points"][k_off] = float("nan"), float("inf")
+        a["tau"][q_off] = float("nan")
+    out, lse = msda.msda_query_attention(**a)
+    check_forward(a, out, lse)
+    do = torch.randn(B, Nq, H * 32, device="cuda").bfloat16()
+    do[q_off] = float("nan")
+    grads = msda.msda_query_attention_backward(**a, lse=lse, grad_out=do)
+    assert all(t is None or bool(torch.isfinite(t).all()) for t in grads)
+    assert bool((grads[0][q_off] == 0).all())
+    assert bool((grads[1][k_off] == 0).all()) and bool((grads[2][k_off] == 0).all())
+    check_backward(a, do, grads)
+
+
 @pytest.mark.parametrize("bias,groups", [(False, None), (True, "shared")])
 def test_gradient_against_differences(bias, groups):
     a = problem(1, 20, 30, 2, bias, groups, 8)

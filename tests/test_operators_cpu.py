@@ -7,6 +7,7 @@ import math
 
 import numpy as np
 import pytest
+import torch
 
 import scale_deformable_attention_03_b200 as msda
 from scale_deformable_attention_03_b200 import build as msda_build
@@ -230,6 +231,23 @@ def test_attention_rejects_bad_outputs(L, kw, code):
 def test_attention_backward_rejects_bad_outputs(L, kw, code):
     p = _attention(q_points=FAKE, k_points=FAKE, tau=FAKE)
     assert _attend_back(L, p, **kw) == code
+
+
+def test_attention_backward_rejects_grad_tau_without_tau(L):
+    assert _attend_back(L, _attention()) == INVALID
+    assert "grad_tau without tau" in L.msda_last_error().decode()
+
+
+def test_layouts_are_compared_by_format_not_by_stride():
+    """Of a 1 x 1 kernel's weight in channels-last memory the strides differ, the order does not."""
+    w = torch.empty(8, 6, 1, 1)
+    last = torch.empty_like(w, memory_format=torch.channels_last)
+    odd = torch.empty_strided((8, 6, 1, 1), (6, 1, 6, 6))
+    wide = torch.empty(8, 6, 3, 3)
+    wide_last = wide.to(memory_format=torch.channels_last)
+    same = msda._same_dense_layout
+    assert same(w, last) and same(w, odd) and same(odd, last) and same(wide_last, wide_last)
+    assert not same(wide, wide_last) and not same(wide[:, ::2], wide[:, ::2])
 
 
 def test_attention_of_nothing(L):
