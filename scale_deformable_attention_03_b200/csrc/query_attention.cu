@@ -359,7 +359,7 @@ cudaError_t run(const ForwardArgs& a, cudaStream_t s)
 
 }  // namespace
 
-Plan plan_of(int B, int Nq, int Nk, int H, bool bias, int blocks)
+Plan plan_of(int B, int Nq, int Nk, int H, bool bias, bool groups, int blocks)
 {
     Plan p;
     const int64_t wave = blocks * kSms;
@@ -371,7 +371,7 @@ Plan plan_of(int B, int Nq, int Nk, int H, bool bias, int blocks)
     if (splits <= 1) {
         // waves in units of a whole one, 2 % of a wave for each split's join
         double least = 1e30;
-        for (int s = 1; s == 1 || (s <= 4 && tiles / s >= kEvenTiles); ++s) {
+        for (int s = 1; s == 1 || (!groups && s <= 4 && tiles / s >= kEvenTiles); ++s) {
             const double cost = (double)((ctas * s + wave - 1) / wave) / s + 0.02 * (s - 1);
             if (cost < least) {
                 least = cost;
@@ -499,7 +499,8 @@ extern "C" msda_status_t msda_query_attention(const msda_attention_t* p, void* o
     if (touches_inputs(p, out, (size_t)p->B * p->Nq * p->H * kDim * 2) ||
         touches_inputs(p, lse, (size_t)p->B * p->Nq * p->H * 4))
         return api_fail(MSDA_ERR_INVALID_ARG, "out or lse overlaps q, k or v");
-    const Plan plan = plan_of(p->B, p->Nq, p->Nk, p->H, p->tau != nullptr, kBlocks);
+    const Plan plan = plan_of(p->B, p->Nq, p->Nk, p->H, p->tau != nullptr,
+                              p->q_group || p->k_group, kBlocks);
     ForwardArgs a;
     a.in = inputs_of(*p);
     a.out = static_cast<__nv_bfloat16*>(out);

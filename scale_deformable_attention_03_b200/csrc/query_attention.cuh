@@ -485,11 +485,14 @@ constexpr int kSms = 148;
 // and shorter CTAs are faster).  The keys are split until the CTAs fill a wave,
 // down to two tiles per CTA, and of long rows where it evens out the last wave:
 // 628 CTAs in waves of 592 take two of them (704 us for the 100 x 100 grid),
-// quartered they take five a quarter as long (580 us).
+// quartered they take five a quarter as long (580 us).  With groups only the fill
+// counts: the tiles that a CTA needs are few and lie together, and parts of a row
+// without any still look them up (10 000 queries in seven documents one after the
+// other: 244 us, with even waves 398 us; in one shared group 783 against 636 us).
 struct Plan {
     int heads, splits, split_tiles;
 };
-Plan plan_of(int B, int Nq, int Nk, int H, bool bias, int blocks);
+Plan plan_of(int B, int Nq, int Nk, int H, bool bias, bool groups, int blocks);
 
 // Device copy of the inputs.
 struct Inputs {
