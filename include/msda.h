@@ -652,7 +652,8 @@ typedef struct {
  *   out [B, Nq, H * 32] bf16, written
  *   lse [B, H, Nq]      fp32, written; for the backward (NULL: not wanted)
  * The products are exact and accumulate in fp32, softmax and sums are fp32;
- * the weights are rounded to bf16 for their product with v.  q, k, v and out
+ * the weights are rounded to bf16 for their product with v (to 16 bits for up to
+ * 1024 queries times heads times items).  q, k, v and out
  * 16-byte aligned, points 8-byte. */
 msda_status_t msda_query_attention(const msda_attention_t* p, void* out, float* lse,
                                    msda_stream_t stream);
@@ -667,7 +668,8 @@ msda_status_t msda_query_attention(const msda_attention_t* p, void* out, float* 
  *   grad_out [B, Nq, H * 32] bf16
  *   grad_q [B, Nq, H, 32], grad_k and grad_v [B, Nk, H, 32] bf16, contiguous,
  *   written; grad_tau [B, Nq, H] fp32, written (NULL where p->tau is)
- * p and ds are rounded to bf16 for the products with grad_out, k and q; the
+ * p and ds are rounded to bf16 for the products with grad_out, k and q (to 16
+ * bits for gradients of up to 1024 rows of a head); the
  * sum over j of p dp is formed in fp32 from the unrounded values.  Alignment
  * as in the forward; workspace >= msda_query_attention_backward_workspace_size(p)
  * bytes (which looks at B, Nq and H), 256-byte aligned, contents ignored. */

@@ -61,7 +61,7 @@ __device__ __forceinline__ void load_keys(ForwardSmem<HP>& sm, int stage, const 
     cp_commit();
 }
 
-template <int HP, bool kBias, bool kGroups>
+template <int HP, bool kBias, bool kGroups, bool kExact>
 __global__ void __launch_bounds__(kAttnThreads, kBlocks)
     attention_forward_kernel(const ForwardArgs a)
 {
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocks)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     // the weights in bf16: the matrix instruction's type, v's own; 2^-8 of
-                    // each at most, what out's own rounding may be
+                    // each at most, what out's own rounding may be (with kExact 2^-16)
                     const uint32_t pf[4] = {pack_bf16(s[2 * k][0]), pack_bf16(s[2 * k][1]),
                                             pack_bf16(s[2 * k + 1][0]),
                                             pack_bf16(s[2 * k + 1][1])};
@@ -263,6 +263,14 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocks)
                         load_sum(r, sv, 2 * part + k, d, lanes);
                         mma(o[hh][2 * d], pf, r[0], r[1]);
                         mma(o[hh][2 * d + 1], pf, r[2], r[3]);
+                        if constexpr (kExact) {
+                            const uint32_t pr[4] = {pack_rest(s[2 * k][0], pf[0]),
+                                                    pack_rest(s[2 * k][1], pf[1]),
+                                                    pack_rest(s[2 * k + 1][0], pf[2]),
+                                                    pack_rest(s[2 * k + 1][1], pf[3])};
+                            mma(o[hh][2 * d], pr, r[0], r[1]);
+                            mma(o[hh][2 * d + 1], pr, r[2], r[3]);
+                        }
                     }
                 }
                 if (!ends) scores(stage, (u + 1) / HP, (u + 1) % HP, tile);
@@ -346,10 +354,10 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocks)
     cluster_sync();  // nobody's shared memory goes while others read it
 }
 
-template <int HP, bool kBias, bool kGroups>
+template <int HP, bool kBias, bool kGroups, bool kExact>
 cudaError_t run(const ForwardArgs& a, cudaStream_t s)
 {
-    constexpr auto kernel = attention_forward_kernel<HP, kBias, kGroups>;
+    constexpr auto kernel = attention_forward_kernel<HP, kBias, kGroups, kExact>;
     const cudaError_t e = allow_shared<kernel>(sizeof(ForwardSmem<HP>));
     if (e != cudaSuccess) return e;
     const int64_t ctas = (int64_t)a.q_tiles * a.in.B * (a.in.H / HP) * a.splits;
@@ -510,8 +518,14 @@ extern "C" msda_status_t msda_query_attention(const msda_attention_t* p, void* o
     a.split_tiles = plan.split_tiles;
     const cudaStream_t s = (cudaStream_t)stream;
     const bool groups = p->q_group || p->k_group;
-    const auto call = plan.heads == 2 ? (groups ? run<2, true, true> : run<2, true, false>)
-                      : p->tau        ? (groups ? run<1, true, true> : run<1, true, false>)
-                                      : (groups ? run<1, false, true> : run<1, false, false>);
+    using Run = cudaError_t (*)(const ForwardArgs&, cudaStream_t);
+    static constexpr Run runs[8] = {
+        run<1, false, false, false>, run<1, false, false, true>, run<1, false, true, false>,
+        run<1, false, true, true>,   run<1, true, false, false>, run<1, true, false, true>,
+        run<1, true, true, false>,   run<1, true, true, true>};
+    const Run call = plan.heads == 2
+                         ? (groups ? run<2, true, true, false> : run<2, true, false, false>)
+                         : runs[4 * (p->tau != nullptr) + 2 * groups +
+                                exact_of((int64_t)p->B * p->Nq * p->H)];
     return api_cuda(call(a, s), "msda_query_attention");
 }

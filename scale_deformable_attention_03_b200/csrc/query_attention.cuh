@@ -83,6 +83,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// What pack_bf16's rounding left over, packed likewise.
+__device__ __forceinline__ uint32_t pack_rest(float2 v, uint32_t packed)
+{
+    return pack_bf16(v.x - __uint_as_float(packed << 16),
+                     v.y - __uint_as_float(packed & 0xffff0000u));
+}
+
 // c += a b for a 16 x 16 by 16 x 8 product.
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t* a, uint32_t b0, uint32_t b1)
 {
@@ -492,6 +499,17 @@ constexpr int kSms = 148;
 struct Plan {
     int heads, splits, split_tiles;
 };
+
+// Whether the weights (and ds, in the gradient) keep 16 bits, as two bf16 in two
+// products, instead of 8.  With 8 bits an output is off by sqrt(2) of its own
+// rounding on average; over thousands of rows that is what it is, among the few of a
+// decoding step a single one stands out.  Those leave most of the GPU idle, so
+// that the second product costs them least: one query over 4097 keys, 16 heads,
+// 14.3 us on the GPU instead of 13.5; 7200 rows (900 queries) 15.6 instead of 13.1 and
+// the gradient of 5000 queries a fifth more, which they are spared.
+constexpr int64_t kExactRows = 1024;
+inline bool exact_of(int64_t rows) { return rows <= kExactRows; }
+
 Plan plan_of(int B, int Nq, int Nk, int H, bool bias, bool groups, int blocks);
 
 // Device copy of the inputs.

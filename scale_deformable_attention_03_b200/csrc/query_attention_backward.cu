@@ -36,6 +36,7 @@ struct BackwardArgs {
     float* dtau;
     float* rows;  // [3, B, H, Nq]: -lse and -tau in units of log 2, D
     int q_tiles, k_tiles, splits, split_tiles;
+    bool exact_q, exact_k;  // of dq; of dk and dv
 };
 
 template <int HP>
@@ -102,10 +103,10 @@ __device__ __forceinline__ void products(float2 (&c)[4][2], const uint32_t (&f)[
     }
 }
 
-// acc += w (16 x 32, rounded to bf16: the matrix instruction's type) times the
-// tile's rows 32s .. 32s + 31.
+// acc += w (16 x 32, rounded to bf16: the matrix instruction's type; what that leaves
+// over in a second product with `exact`) times the tile's rows 32s .. 32s + 31.
 __device__ __forceinline__ void accumulate(float (&acc)[4][4], const float2 (&w)[4][2],
-                                           uint32_t tile, int s, const LaneAt& lanes)
+                                           uint32_t tile, int s, const LaneAt& lanes, bool exact)
 {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -117,6 +118,13 @@ __device__ __forceinline__ void accumulate(float (&acc)[4][4], const float2 (&w)
             load_sum(r, tile, 2 * s + k, d, lanes);
             mma(acc[2 * d], f, r[0], r[1]);
             mma(acc[2 * d + 1], f, r[2], r[3]);
+            if (exact) {
+                const uint32_t e[4] = {pack_rest(w[2 * k][0], f[0]), pack_rest(w[2 * k][1], f[1]),
+                                       pack_rest(w[2 * k + 1][0], f[2]),
+                                       pack_rest(w[2 * k + 1][1], f[3])};
+                mma(acc[2 * d], e, r[0], r[1]);
+                mma(acc[2 * d + 1], e, r[2], r[3]);
+            }
         }
     }
 }
@@ -149,7 +157,7 @@ __device__ __forceinline__ float quad_sum(float x)
 
 // 64 queries and the tiles [begin, last) of the keys: D (and what the last
 // kernel needs of the queries beside it), or with kGrad, given D, dq and dtau.
-template <int HP, bool kBias, bool kGroups, bool kGrad>
+template <int HP, bool kBias, bool kGroups, bool kGrad, bool kExact>
 __device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardArgs& a, int id,
                                           int split)
 {
@@ -312,7 +320,7 @@ __device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardAr
                         }
                         dt[hh][0] += sum[0].x + sum[0].y;
                         dt[hh][1] += sum[1].x + sum[1].y;
-                        accumulate(dq[hh], s, sk, st, lanes);
+                        accumulate(dq[hh], s, sk, st, lanes, kExact && a.exact_q);
                     }
                 }
             }
@@ -365,7 +373,7 @@ __device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardAr
 }
 
 // 64 keys and all queries: dk and dv.
-template <int HP, bool kBias, bool kGroups>
+template <int HP, bool kBias, bool kGroups, bool kExact>
 __device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const BackwardArgs& a, int id)
 {
     const Inputs& in = a.in;
@@ -482,8 +490,8 @@ __device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const Backwar
                             if (!clear) mask(dp[j][half], hide >> (4 * j + 2 * half), 0.0f);
                         }
                     }
-                    accumulate(dv[hh], s, so, st, lanes);
-                    accumulate(dk[hh], dp, sq, st, lanes);
+                    accumulate(dv[hh], s, so, st, lanes, kExact && a.exact_k);
+                    accumulate(dk[hh], dp, sq, st, lanes, kExact && a.exact_k);
                 }
             }
             __syncthreads();
@@ -503,16 +511,16 @@ __global__ void __launch_bounds__(kAttnThreads, kDotBlocks) attention_dots_kerne
 {
     __shared__ BackwardSmem<HP> sm;
     const int id = blockIdx.x / a.splits;
-    walk_keys<HP, kBias, kGroups, false>(sm, a, id, blockIdx.x - id * a.splits);
+    walk_keys<HP, kBias, kGroups, false, false>(sm, a, id, blockIdx.x - id * a.splits);
 }
 
-template <bool kBias, bool kGroups>
+template <bool kBias, bool kGroups, bool kExact>
 __global__ void __launch_bounds__(kAttnThreads, kBlocks) attention_grad_kernel(const BackwardArgs a)
 {
     __shared__ BackwardSmem<1> sm;
     const int keys = a.k_tiles * a.in.H * a.in.B;  // the longer ones first
-    if ((int)blockIdx.x < keys) walk_queries<1, kBias, kGroups>(sm, a, blockIdx.x);
-    else walk_keys<1, kBias, kGroups, true>(sm, a, blockIdx.x - keys, 0);
+    if ((int)blockIdx.x < keys) walk_queries<1, kBias, kGroups, kExact>(sm, a, blockIdx.x);
+    else walk_keys<1, kBias, kGroups, true, kExact>(sm, a, blockIdx.x - keys, 0);
 }
 
 template <bool kGroups>
@@ -529,8 +537,12 @@ cudaError_t run(const BackwardArgs& a, const Plan& plan, bool bias, cudaStream_t
         if (e != cudaSuccess) return e;
     }
     const unsigned ctas = (unsigned)(items * (a.q_tiles + a.k_tiles));
-    if (bias) attention_grad_kernel<true, kGroups><<<ctas, kAttnThreads, 0, s>>>(a);
-    else attention_grad_kernel<false, kGroups><<<ctas, kAttnThreads, 0, s>>>(a);
+    const bool exact = a.exact_q || a.exact_k;
+    const auto grads = bias ? (exact ? attention_grad_kernel<true, kGroups, true>
+                                     : attention_grad_kernel<true, kGroups, false>)
+                            : (exact ? attention_grad_kernel<false, kGroups, true>
+                                     : attention_grad_kernel<false, kGroups, false>);
+    grads<<<ctas, kAttnThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -594,6 +606,8 @@ extern "C" msda_status_t msda_query_attention_backward(const msda_attention_t* p
     a.split_tiles = plan.split_tiles;
     a.q_tiles = (p->Nq + kTile - 1) / kTile;
     a.k_tiles = (p->Nk + kTile - 1) / kTile;
+    a.exact_q = exact_of((int64_t)p->B * p->Nq * p->H);
+    a.exact_k = exact_of((int64_t)p->B * p->Nk * p->H);
     const cudaStream_t s = (cudaStream_t)stream;
     const bool bias = p->tau != nullptr;
     const cudaError_t e = p->q_group || p->k_group ? run<true>(a, plan, bias, s)
