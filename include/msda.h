@@ -669,7 +669,7 @@ msda_status_t msda_query_attention(const msda_attention_t* p, void* out, float* 
  *   grad_q [B, Nq, H, 32], grad_k and grad_v [B, Nk, H, 32] bf16, contiguous,
  *   written; grad_tau [B, Nq, H] fp32, written (NULL where p->tau is)
  * p and ds are rounded to bf16 for the products with grad_out, k and q (to 16
- * bits for gradients of up to 1024 rows of a head); the
+ * bits for up to 1024 rows times heads times items on one side); the
  * sum over j of p dp is formed in fp32 from the unrounded values.  Alignment
  * as in the forward; workspace >= msda_query_attention_backward_workspace_size(p)
  * bytes (which looks at B, Nq and H), 256-byte aligned, contents ignored. */

@@ -36,7 +36,6 @@ struct BackwardArgs {
     float* dtau;
     float* rows;  // [3, B, H, Nq]: -lse and -tau in units of log 2, D
     int q_tiles, k_tiles, splits, split_tiles;
-    bool exact_q, exact_k;  // of dq; of dk and dv
 };
 
 template <int HP>
@@ -104,9 +103,10 @@ __device__ __forceinline__ void products(float2 (&c)[4][2], const uint32_t (&f)[
 }
 
 // acc += w (16 x 32, rounded to bf16: the matrix instruction's type; what that leaves
-// over in a second product with `exact`) times the tile's rows 32s .. 32s + 31.
+// over in a second product with kExact) times the tile's rows 32s .. 32s + 31.
+template <bool kExact>
 __device__ __forceinline__ void accumulate(float (&acc)[4][4], const float2 (&w)[4][2],
-                                           uint32_t tile, int s, const LaneAt& lanes, bool exact)
+                                           uint32_t tile, int s, const LaneAt& lanes)
 {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -118,7 +118,7 @@ __device__ __forceinline__ void accumulate(float (&acc)[4][4], const float2 (&w)
             load_sum(r, tile, 2 * s + k, d, lanes);
             mma(acc[2 * d], f, r[0], r[1]);
             mma(acc[2 * d + 1], f, r[2], r[3]);
-            if (exact) {
+            if constexpr (kExact) {
                 const uint32_t e[4] = {pack_rest(w[2 * k][0], f[0]), pack_rest(w[2 * k][1], f[1]),
                                        pack_rest(w[2 * k + 1][0], f[2]),
                                        pack_rest(w[2 * k + 1][1], f[3])};
@@ -320,7 +320,7 @@ __device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardAr
                         }
                         dt[hh][0] += sum[0].x + sum[0].y;
                         dt[hh][1] += sum[1].x + sum[1].y;
-                        accumulate(dq[hh], s, sk, st, lanes, kExact && a.exact_q);
+                        accumulate<kExact>(dq[hh], s, sk, st, lanes);
                     }
                 }
             }
@@ -490,8 +490,8 @@ __device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const Backwar
                             if (!clear) mask(dp[j][half], hide >> (4 * j + 2 * half), 0.0f);
                         }
                     }
-                    accumulate(dv[hh], s, so, st, lanes, kExact && a.exact_k);
-                    accumulate(dk[hh], dp, sq, st, lanes, kExact && a.exact_k);
+                    accumulate<kExact>(dv[hh], s, so, st, lanes);
+                    accumulate<kExact>(dk[hh], dp, sq, st, lanes);
                 }
             }
             __syncthreads();
@@ -537,7 +537,8 @@ cudaError_t run(const BackwardArgs& a, const Plan& plan, bool bias, cudaStream_t
         if (e != cudaSuccess) return e;
     }
     const unsigned ctas = (unsigned)(items * (a.q_tiles + a.k_tiles));
-    const bool exact = a.exact_q || a.exact_k;
+    // (few rows on one side: a gradient of the other is made of few terms)
+    const bool exact = exact_of((int64_t)a.in.B * a.in.H * std::min(a.in.Nq, a.in.Nk));
     const auto grads = bias ? (exact ? attention_grad_kernel<true, kGroups, true>
                                      : attention_grad_kernel<true, kGroups, false>)
                             : (exact ? attention_grad_kernel<false, kGroups, true>
@@ -606,8 +607,6 @@ extern "C" msda_status_t msda_query_attention_backward(const msda_attention_t* p
     a.split_tiles = plan.split_tiles;
     a.q_tiles = (p->Nq + kTile - 1) / kTile;
     a.k_tiles = (p->Nk + kTile - 1) / kTile;
-    a.exact_q = exact_of((int64_t)p->B * p->Nq * p->H);
-    a.exact_k = exact_of((int64_t)p->B * p->Nk * p->H);
     const cudaStream_t s = (cudaStream_t)stream;
     const bool bias = p->tau != nullptr;
     const cudaError_t e = p->q_group || p->k_group ? run<true>(a, plan, bias, s)
