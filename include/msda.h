@@ -578,9 +578,12 @@ typedef enum {
  *   gamma, beta [L, C]       fp32; NULL: 1 and 0
  *   y           [B, Nv, C]   fp32 or bf16 (y_dtype), written; not x
  *   mean, rstd  [B, L, G]    fp32, written; for the backward (NULL: not wanted)
- * The statistics are accumulated relative to values of the data and merged in
- * double (no cancellation when the mean is far from zero), and the same on
- * every run; values of a channel differ by less than 1e16 (fp32 squares).  eps: finite, > 0.  x, y, gamma and beta 16-byte aligned;
+ * The statistics are summed in fp32 over eight rows of a channel at a time,
+ * relative to the first of the eight, and in double beyond: wherever the mean
+ * lies and however far single rows lie from it, rstd is off by less than 2^-16
+ * of itself and the mean by less than 2^-19 spreads and its rounding.  The same
+ * on every run; values of a channel differ by less than 1e16 (fp32 squares).
+ * eps: finite, > 0.  x, y, gamma and beta 16-byte aligned;
  * workspace >= msda_group_norm_workspace_size(d) bytes, 256-byte aligned,
  * contents ignored. */
 size_t msda_group_norm_workspace_size(msda_norm_dims_t d);

@@ -27,7 +27,7 @@
 //
 // Bound by memory: the rows are read twice, the second time from L2 as far as
 // that reaches, and written once.  Six cameras (185 k rows of 256, fp32 to bf16):
-// 83 us, 473 MB at 5.7 TB/s with next to nothing left in L2 for the second pass;
+// 85 us, 473 MB at 5.5 TB/s with next to nothing left in L2 for the second pass;
 // taking the cameras in twos, so that a pass fits, costs as much in the ends of
 // its launches as it saves.  The gradient of the same in fp32: 162 us, 946 MB at
 // 5.8 TB/s.
@@ -244,9 +244,14 @@ struct RowCopy {
     }
 };
 
+// Rows of a thread whose sums are formed in fp32 before they join a double.
+constexpr int kBlockRows = 8;
+
 // Walks a thread's `count` rows, `step` values apart from the one that starts
 // at `first` on, through the ring: start() asks for the first steps, run()
-// calls use(row, x) or use(row, x, dy) for every row.
+// calls use(row, x) or use(row, x, dy) for every row.  run_blocks() takes the
+// rows in blocks of kBlockRows: use(x, leads) for each, `leads` for a block's
+// first, and join(rows) behind a block.
 template <bool kX, bool kSplit>
 struct Walk1 {
     using Copy = RowCopy<kX, kSplit>;
@@ -284,6 +289,23 @@ struct Walk1 {
             for (int i = 0; i < kRows; ++i)
                 if (k * kRows + i < count)
                     use(first + (int64_t)(k * kRows + i) * step, Copy::take(at(k, i)));
+        }
+    }
+    template <typename F, typename J>
+    __device__ __forceinline__ void run_blocks(F use, J join) const
+    {
+        for (int row = 0; row < count; row += kBlockRows) {
+#pragma unroll
+            for (int r = 0; r < kBlockRows; r += kRows) {
+                if (row + r >= count) break;
+                const int k = (row + r) / kRows;
+                ask(k + kStages - 1);
+                copy_wait();
+#pragma unroll
+                for (int i = 0; i < kRows; ++i)
+                    if (row + r + i < count) use(Copy::take(at(k, i)), r + i == 0);
+            }
+            join(min(kBlockRows, count - row));
         }
     }
 };
@@ -350,7 +372,7 @@ __device__ __forceinline__ Vec8 load_channels(const float* p, int64_t row, const
 // Adds the slots' sums of two quantities per channel: on return s[0][0][c] and
 // s[1][0][c] hold the chunk's sums of channel c (for the thread that owns it,
 // threads c mod kNormThreads; a barrier before others read them).
-__device__ __forceinline__ void add_slots(float* s, int C, int slots)
+__device__ __forceinline__ void add_slots_f(float* s, int C, int slots)
 {
     __syncthreads();
     float* s2 = s + kNormThreads * 8;
@@ -365,7 +387,7 @@ __device__ __forceinline__ void add_slots(float* s, int C, int slots)
     }
 }
 
-__device__ __forceinline__ void put_slot(float* s, int C, int slot, const Quads& c, const Vec8& a,
+__device__ __forceinline__ void put_slot_f(float* s, int C, int slot, const Quads& c, const Vec8& a,
                                          const Vec8& b)
 {
     float* p = s + slot * C;
@@ -374,6 +396,46 @@ __device__ __forceinline__ void put_slot(float* s, int C, int slot, const Quads&
     *reinterpret_cast<float4*>(p + c.b) = make_float4(a.v[4], a.v[5], a.v[6], a.v[7]);
     *reinterpret_cast<float4*>(q + c.a) = make_float4(b.v[0], b.v[1], b.v[2], b.v[3]);
     *reinterpret_cast<float4*>(q + c.b) = make_float4(b.v[4], b.v[5], b.v[6], b.v[7]);
+}
+
+// The sums of two quantities per channel and slot, in double: they lie where the
+// ring was, whose rows have all been taken behind a barrier.
+constexpr int kSumsPlane = kNormThreads * 8;
+static_assert(2 * kSumsPlane * sizeof(double) <= kRingBytes, "");
+
+__device__ __forceinline__ double* slot_sums() { return reinterpret_cast<double*>(ring_memory); }
+
+struct Sums8 {
+    double v[8];
+};
+
+__device__ __forceinline__ void put_slot(double* s, int C, int slot, const Quads& c,
+                                         const Sums8& a, const Sums8& b)
+{
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const int at = slot * C + channel(c, j);
+        *reinterpret_cast<double2*>(s + at) = make_double2(a.v[j], a.v[j + 1]);
+        *reinterpret_cast<double2*>(s + kSumsPlane + at) = make_double2(b.v[j], b.v[j + 1]);
+    }
+}
+
+// Adds the slots' sums: on return s[c] and s[kSumsPlane + c] hold channel c's (for
+// the thread that owns it, threads c mod kNormThreads; a barrier before others
+// read them).
+__device__ __forceinline__ void add_slots(double* s, int C, int slots)
+{
+    __syncthreads();
+    double* s2 = s + kSumsPlane;
+    for (int c = threadIdx.x; c < C; c += kNormThreads) {
+        double a = s[c], b = s2[c];
+        for (int k = 1; k < slots; ++k) {
+            a += s[k * C + c];
+            b += s2[k * C + c];
+        }
+        s[c] = a;
+        s2[c] = b;
+    }
 }
 
 // The 32 (or fewer) lanes that add up a group of cg channels: a power of two,
@@ -400,10 +462,17 @@ __device__ __forceinline__ double add_lanes(double v, int seg)
 
 // A span's sums of x - m and of its square per group, m the mean of the group's
 // channels in the level's first row: the same for all spans of the level, so
-// that their sums add up, and near enough to the group's mean that nothing
-// cancels.  Within a channel the sums are fp32 and relative to the channel's
-// own value in that row; they are moved to m and added over the channels in
-// double.
+// that their sums add up.  m need not be near the group's mean: with N rows the
+// row that it comes from makes 1 / N of the variance at least, so what cancels
+// is N of the 2^53 of a double at most.  fp32 does not have such room, so it only holds
+// sums of eight rows of a channel, relative to the first of the eight, whose
+// distance from the mean is part of the same sum: they are off by less than 380
+// roundings of the group's sum of squares whatever the data are (2^-16.4 of r).  They
+// are moved to the channel's value in the level's first row, and then to m, in
+// double.  (With all rows of a run summed in fp32 and relative to the level's first
+// row, a blank first pixel under features 300 spreads from zero cost r 1e-3, and the
+// six cameras took 2.7 us less: 1.5 us for the moves, the rest for sums of 64 bits in
+// shared memory.  Blocks of 16 rows: 0.6 us less, and twice the bound.)
 struct SumsSmem {
     alignas(16) float s[2 * kNormThreads * 8];
     float first[kMaxC];
@@ -414,13 +483,16 @@ __device__ __forceinline__ void norm_stats(SumsSmem& sm, const void* __restrict_
                                            const NormShape& n, double2* part, double* middle)
 {
     constexpr bool kSplit = !kX;
-    float *s = sm.s, *first = sm.first;
+    double* s = slot_sums();
+    float* first = sm.first;
     const int slot = threadIdx.x / n.tpr;
     const Quads c = quads_of<kSplit>(n.C, threadIdx.x - slot * n.tpr);
     const GroupLanes gl = group_lanes(n.cg);
     const int64_t end = run_begin(n, blockIdx.x + 1);
     for (int64_t at = run_begin(n, blockIdx.x); at < end;) {
         const Span sp = span_from(n, at, end);
+        Vec8 ref{};
+        Sums8 sum{}, square{};
         if (slot < n.slots) {
             const Walk1<kX, kSplit> walk{ring_memory,
                                          x,
@@ -429,17 +501,36 @@ __device__ __forceinline__ void norm_stats(SumsSmem& sm, const void* __restrict_
                                          (int64_t)n.slots * n.C,
                                          (sp.rows - slot + n.slots - 1) / n.slots};
             walk.start();
-            const Vec8 ref = load8<kX>(x, ((int64_t)sp.b * n.Nv + n.start[sp.l]) * n.C, c);
-            Vec8 a{}, q{};
-            walk.run([&](int64_t, const Vec8& v) {
+            ref = load8<kX>(x, ((int64_t)sp.b * n.Nv + n.start[sp.l]) * n.C, c);
+            Vec8 lead{}, a{}, q{};
+            walk.run_blocks(
+                [&](const Vec8& v, bool leads) {
+                    if (leads) {
+                        lead = v;
+                        a = q = Vec8{};
+                        return;
+                    }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float d = v.v[j] - ref.v[j];
-                    a.v[j] += d;
-                    q.v[j] = fmaf(d, d, q.v[j]);
-                }
-            });
-            put_slot(s, n.C, slot, c, a, q);
+                    for (int j = 0; j < 8; ++j) {
+                        const float d = v.v[j] - lead.v[j];
+                        a.v[j] += d;
+                        q.v[j] = fmaf(d, d, q.v[j]);
+                    }
+                },
+                [&](int rows) {
+                    const double k = (double)rows;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const double d = (double)lead.v[j] - (double)ref.v[j], s1 = (double)a.v[j];
+                        const double moved = fma(k, d, s1);
+                        sum.v[j] += moved;
+                        square.v[j] += fma(d, s1 + moved, (double)q.v[j]);
+                    }
+                });
+        }
+        __syncthreads();  // the ring is free
+        if (slot < n.slots) {
+            put_slot(s, n.C, slot, c, sum, square);
             if (slot == 0) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) first[channel(c, j)] = ref.v[j];
@@ -460,7 +551,7 @@ __device__ __forceinline__ void norm_stats(SumsSmem& sm, const void* __restrict_
                 const int ch = g * n.cg + k;
                 const double a = s[ch], d = (double)first[ch] - m;
                 t1 += a + rows * d;
-                t2 += (double)s[kNormThreads * 8 + ch] + d * (2.0 * a + rows * d);
+                t2 += s[kSumsPlane + ch] + d * (2.0 * a + rows * d);
             }
             t1 = add_lanes(t1, gl.seg);
             t2 = add_lanes(t2, gl.seg);
@@ -754,9 +845,9 @@ __device__ __forceinline__ void norm_grad_sums(SumsSmem& sm, const GradIn& in, c
                     q.v[j] = fmaf(dz, hat, q.v[j]);
                 }
             });
-            put_slot(s, n.C, slot, c, a, q);
+            put_slot_f(s, n.C, slot, c, a, q);
         }
-        add_slots(s, n.C, n.slots);
+        add_slots_f(s, n.C, n.slots);
         __syncthreads();
         const int64_t to = span_slot(blockIdx.x, (int64_t)sp.b * n.L + sp.l);
         for (int ch = threadIdx.x; ch < n.C; ch += kNormThreads) {
