@@ -600,7 +600,9 @@ msda_status_t msda_group_norm(const void* x, msda_dtype_t x_dtype, const int64_t
  *   grad_gamma[l, c] = sum over b and rows of dz xh
  *   grad_beta[l, c]  = sum over b and rows of dz
  *   grad_x = rstd (t - mean(t) - xh mean(t xh)),  t = gamma dz,
- * the means over the group's rows and channels.  Deterministic (no atomics).
+ * the means over the group's rows and channels.  Sums are fp32 over eight rows
+ * of a channel at a time and double beyond, each within 2^-20 of the sum of its
+ * terms' magnitudes.  Deterministic (no atomics).
  *   x, gamma, beta, act as in the forward; mean, rstd [B, L, G] from it
  *   grad_y     [B, Nv, C] fp32 or bf16 (gy_dtype); rows of no level not read
  *   grad_x     [B, Nv, C] fp32 or bf16 (gx_dtype), written, 0 in rows of no

@@ -250,8 +250,8 @@ constexpr int kBlockRows = 8;
 // Walks a thread's `count` rows, `step` values apart from the one that starts
 // at `first` on, through the ring: start() asks for the first steps, run()
 // calls use(row, x) or use(row, x, dy) for every row.  run_blocks() takes the
-// rows in blocks of kBlockRows: use(x, leads) for each, `leads` for a block's
-// first, and join(rows) behind a block.
+// rows in blocks of kBlockRows: use(x, leads) or use(x, dy, leads) for each, `leads`
+// for a block's first, and join(rows) behind a block.
 template <bool kX, bool kSplit>
 struct Walk1 {
     using Copy = RowCopy<kX, kSplit>;
@@ -355,6 +355,25 @@ struct Walk2 {
                         CopyD::take(at(k, i) + CopyX::kPieces * kNormThreads));
         }
     }
+    template <typename F, typename J>
+    __device__ __forceinline__ void run_blocks(F use, J join) const
+    {
+        for (int row = 0; row < count; row += kBlockRows) {
+#pragma unroll
+            for (int r = 0; r < kBlockRows; r += kRows) {
+                if (row + r >= count) break;
+                const int k = (row + r) / kRows;
+                ask(k + kStages - 1);
+                copy_wait();
+#pragma unroll
+                for (int i = 0; i < kRows; ++i)
+                    if (row + r + i < count)
+                        use(CopyX::take(at(k, i)),
+                            CopyD::take(at(k, i) + CopyX::kPieces * kNormThreads), r + i == 0);
+            }
+            join(min(kBlockRows, count - row));
+        }
+    }
 };
 
 extern __shared__ uint4 ring_memory[];
@@ -367,35 +386,6 @@ __device__ __forceinline__ Vec8 load_channels(const float* p, int64_t row, const
 #pragma unroll
     for (int j = 0; j < 8; ++j) o.v[j] = otherwise;
     return o;
-}
-
-// Adds the slots' sums of two quantities per channel: on return s[0][0][c] and
-// s[1][0][c] hold the chunk's sums of channel c (for the thread that owns it,
-// threads c mod kNormThreads; a barrier before others read them).
-__device__ __forceinline__ void add_slots_f(float* s, int C, int slots)
-{
-    __syncthreads();
-    float* s2 = s + kNormThreads * 8;
-    for (int c = threadIdx.x; c < C; c += kNormThreads) {
-        float a = s[c], b = s2[c];
-        for (int k = 1; k < slots; ++k) {
-            a += s[k * C + c];
-            b += s2[k * C + c];
-        }
-        s[c] = a;
-        s2[c] = b;
-    }
-}
-
-__device__ __forceinline__ void put_slot_f(float* s, int C, int slot, const Quads& c, const Vec8& a,
-                                         const Vec8& b)
-{
-    float* p = s + slot * C;
-    float* q = p + kNormThreads * 8;
-    *reinterpret_cast<float4*>(p + c.a) = make_float4(a.v[0], a.v[1], a.v[2], a.v[3]);
-    *reinterpret_cast<float4*>(p + c.b) = make_float4(a.v[4], a.v[5], a.v[6], a.v[7]);
-    *reinterpret_cast<float4*>(q + c.a) = make_float4(b.v[0], b.v[1], b.v[2], b.v[3]);
-    *reinterpret_cast<float4*>(q + c.b) = make_float4(b.v[4], b.v[5], b.v[6], b.v[7]);
 }
 
 // The sums of two quantities per channel and slot, in double: they lie where the
@@ -473,18 +463,12 @@ __device__ __forceinline__ double add_lanes(double v, int seg)
 // row, a blank first pixel under features 300 spreads from zero cost r 1e-3, and the
 // six cameras took 2.7 us less: 1.5 us for the moves, the rest for sums of 64 bits in
 // shared memory.  Blocks of 16 rows: 0.6 us less, and twice the bound.)
-struct SumsSmem {
-    alignas(16) float s[2 * kNormThreads * 8];
-    float first[kMaxC];
-};
-
 template <bool kX>
-__device__ __forceinline__ void norm_stats(SumsSmem& sm, const void* __restrict__ x,
+__device__ __forceinline__ void norm_stats(float* first, const void* __restrict__ x,
                                            const NormShape& n, double2* part, double* middle)
 {
     constexpr bool kSplit = !kX;
     double* s = slot_sums();
-    float* first = sm.first;
     const int slot = threadIdx.x / n.tpr;
     const Quads c = quads_of<kSplit>(n.C, threadIdx.x - slot * n.tpr);
     const GroupLanes gl = group_lanes(n.cg);
@@ -722,9 +706,9 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_stats_kernel(const void*
                                                                      double2* __restrict__ part,
                                                                      double* __restrict__ middle)
 {
-    __shared__ SumsSmem sm;
+    __shared__ float first[kMaxC];
     pdl_trigger();
-    norm_stats<kX>(sm, x, n, part, middle);
+    norm_stats<kX>(first, x, n, part, middle);
 }
 
 // (no __restrict__ on what the first pass writes while this one has begun)
@@ -747,10 +731,10 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_small_kernel(const void*
                                                                      const NormOut out)
 {
     __shared__ union {
-        SumsSmem sums;
+        float first[kMaxC];
         ApplySmem apply;
     } sm;
-    norm_stats<kX>(sm.sums, x, n, part, middle);
+    norm_stats<kX>(sm.first, x, n, part, middle);
     cluster_sync();
     norm_apply<kX, kY, kAct>(sm.apply, x, n, part, middle, out, blockIdx.x, [] {});
 }
@@ -798,8 +782,10 @@ __device__ __forceinline__ Channels load_constants(const NormShape& n, int b, in
     return k;
 }
 
-// A span's sums of dz and dz xh per channel (fp32, for the parameters'
-// gradients) and, weighted with gamma, per group (double, for dx).
+// A span's sums of dz and dz xh per channel (for the parameters' gradients) and,
+// weighted with gamma, per group (for dx): fp32 over eight rows, double beyond.  A
+// loss that is a mean has gradients of one sign and size, whose roundings in a long
+// fp32 sum do not cancel (830 rows: 1e-5 of the sum).
 struct GradIn {
     const void *x, *dy;
     const float *mean, *rstd, *gamma, *beta;
@@ -811,19 +797,20 @@ struct GradOut {
 };
 
 template <bool kX, bool kDy, int kAct>
-__device__ __forceinline__ void norm_grad_sums(SumsSmem& sm, const GradIn& in, const NormShape& n,
+__device__ __forceinline__ void norm_grad_sums(const GradIn& in, const NormShape& n,
                                                float* chan, double2* part)
 {
     constexpr bool kSplit = !(kX && kDy);
     const void *__restrict__ x = in.x, *__restrict__ dy = in.dy;
     const float *mean = in.mean, *rstd = in.rstd, *gamma = in.gamma, *beta = in.beta;
-    float* s = sm.s;
+    double* s = slot_sums();
     const int slot = threadIdx.x / n.tpr;
     const Quads c = quads_of<kSplit>(n.C, threadIdx.x - slot * n.tpr);
     const GroupLanes gl = group_lanes(n.cg);
     const int64_t end = run_begin(n, blockIdx.x + 1);
     for (int64_t at = run_begin(n, blockIdx.x); at < end;) {
         const Span sp = span_from(n, at, end);
+        Sums8 sum{}, product{};
         if (slot < n.slots) {
             const Walk2<kX, kDy, kSplit> walk{ring_memory,
                                               x,
@@ -835,24 +822,34 @@ __device__ __forceinline__ void norm_grad_sums(SumsSmem& sm, const GradIn& in, c
             walk.start();
             const Channels k = load_constants(n, sp.b, sp.l, c, mean, rstd, gamma, beta);
             Vec8 a{}, q{};
-            walk.run([&](int64_t, const Vec8& v, const Vec8& d) {
+            walk.run_blocks(
+                [&](const Vec8& v, const Vec8& d, bool) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float hat = (v.v[j] - k.mean.v[j]) * k.rstd.v[j];
-                    const float dz = grad_z<kAct>(d.v[j], v.v[j], k.mean.v[j], k.rstd.v[j], hat,
-                                                  k.gamma.v[j], k.beta.v[j]);
-                    a.v[j] += dz;
-                    q.v[j] = fmaf(dz, hat, q.v[j]);
-                }
-            });
-            put_slot_f(s, n.C, slot, c, a, q);
+                    for (int j = 0; j < 8; ++j) {
+                        const float hat = (v.v[j] - k.mean.v[j]) * k.rstd.v[j];
+                        const float dz = grad_z<kAct>(d.v[j], v.v[j], k.mean.v[j], k.rstd.v[j],
+                                                      hat, k.gamma.v[j], k.beta.v[j]);
+                        a.v[j] += dz;
+                        q.v[j] = fmaf(dz, hat, q.v[j]);
+                    }
+                },
+                [&](int) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        sum.v[j] += (double)a.v[j];
+                        product.v[j] += (double)q.v[j];
+                    }
+                    a = q = Vec8{};
+                });
         }
-        add_slots_f(s, n.C, n.slots);
+        __syncthreads();  // the ring is free
+        if (slot < n.slots) put_slot(s, n.C, slot, c, sum, product);
+        add_slots(s, n.C, n.slots);
         __syncthreads();
         const int64_t to = span_slot(blockIdx.x, (int64_t)sp.b * n.L + sp.l);
         for (int ch = threadIdx.x; ch < n.C; ch += kNormThreads) {
-            chan[to * 2 * n.C + ch] = s[ch];
-            chan[to * 2 * n.C + n.C + ch] = s[kNormThreads * 8 + ch];
+            chan[to * 2 * n.C + ch] = (float)s[ch];
+            chan[to * 2 * n.C + n.C + ch] = (float)s[kSumsPlane + ch];
         }
         for (int g0 = (threadIdx.x >> 5) * gl.per_warp; g0 < n.G; g0 += kNormWarps * gl.per_warp) {
             const int g = g0 + gl.sub;
@@ -861,8 +858,8 @@ __device__ __forceinline__ void norm_grad_sums(SumsSmem& sm, const GradIn& in, c
             for (int k = gl.in; on && k < n.cg; k += gl.seg) {
                 const int ch = g * n.cg + k;
                 const double w = gamma ? (double)__ldg(gamma + (int64_t)sp.l * n.C + ch) : 1.0;
-                t1 += w * (double)s[ch];
-                t2 += w * (double)s[kNormThreads * 8 + ch];
+                t1 += w * s[ch];
+                t2 += w * s[kSumsPlane + ch];
             }
             t1 = add_lanes(t1, gl.seg);
             t2 = add_lanes(t2, gl.seg);
@@ -988,9 +985,8 @@ template <bool kX, bool kDy, int kAct>
 __global__ void __launch_bounds__(kNormThreads, 2) norm_grad_sums_kernel(
     const GradIn in, const NormShape n, float* __restrict__ chan, double2* __restrict__ part)
 {
-    __shared__ SumsSmem sm;
     pdl_trigger();
-    norm_grad_sums<kX, kDy, kAct>(sm, in, n, chan, part);
+    norm_grad_sums<kX, kDy, kAct>(in, n, chan, part);
 }
 
 // The CTAs behind the runs take a block of the parameters' gradients each.
@@ -1016,16 +1012,13 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_grad_small_kernel(const 
                                                                           double2* part,
                                                                           const GradOut out)
 {
-    __shared__ union {
-        SumsSmem sums;
-        GradSmem grad;
-    } sm;
-    norm_grad_sums<kX, kDy, kAct>(sm.sums, in, n, chan, part);
+    __shared__ GradSmem sm;
+    norm_grad_sums<kX, kDy, kAct>(in, n, chan, part);
     cluster_sync();
-    norm_grad_apply<kX, kDy, kDx, kAct>(sm.grad, in, n, part, out, blockIdx.x, [] {});
+    norm_grad_apply<kX, kDy, kDx, kAct>(sm, in, n, part, out, blockIdx.x, [] {});
     for (int i = blockIdx.x; i < parameter_blocks(n); i += gridDim.x) {
         __syncthreads();  // the shares are free
-        parameter_block(sm.grad.shares, chan, n, i, out);
+        parameter_block(sm.shares, chan, n, i, out);
     }
 }
 
