@@ -656,6 +656,10 @@ typedef struct {
  * everybody sees everything.
  *   out [B, Nq, H * 32] bf16, written
  *   lse [B, H, Nq]      fp32, written; for the backward (NULL: not wanted)
+ * Scores may be of any size as long as both their terms, divided by scale, stay
+ * in fp32's range: the key with a row's highest score has the weight 1 before
+ * the division by their sum, so a tau of 1e10 cuts off all but the nearest key.
+ * As every fp32 score, they are off by some 2^-24 of their terms.
  * The products are exact and accumulate in fp32, softmax and sums are fp32;
  * the weights are rounded to bf16 for their product with v (to 16 bits for up to
  * 1024 queries times heads times items).  q, k, v and out
@@ -673,6 +677,9 @@ msda_status_t msda_query_attention(const msda_attention_t* p, void* out, float* 
  *   grad_out [B, Nq, H * 32] bf16
  *   grad_q [B, Nq, H, 32], grad_k and grad_v [B, Nk, H, 32] bf16, contiguous,
  *   written; grad_tau [B, Nq, H] fp32, written (NULL where p->tau is)
+ * lse is fp32, so p is off by some 2^-23 |lse| of itself; the key that lse comes
+ * from keeps its weight at any size, but among scores past 1e7 a row's other
+ * weights are lost in lse's rounding.
  * p and ds are rounded to bf16 for the products with grad_out, k and q (to 16
  * bits for up to 1024 rows times heads times items on one side); the
  * sum over j of p dp is formed in fp32 from the unrounded values.  Alignment

@@ -45,7 +45,7 @@ struct ForwardSmem {
     alignas(128) unsigned char k[kStages][HP * kTileBytes];
     alignas(128) unsigned char v[kStages][HP * kTileBytes];
     Points pos[kStages];
-    int32_t group[kStages][kTile];
+    alignas(8) int32_t group[kStages][kTile];
     TileBits bits;
 };
 
@@ -61,66 +61,47 @@ __device__ __forceinline__ void load_keys(ForwardSmem<HP>& sm, int stage, const 
     cp_commit();
 }
 
-template <int HP, bool kBias, bool kGroups, bool kExact>
-__global__ void __launch_bounds__(kAttnThreads, kBlocks)
-    attention_forward_kernel(const ForwardArgs a)
+// The queries of a warp (`row` the thread's first) and the tiles [begin, last) of the
+// keys: the sums o of weighted values and l of weights (a thread's own), relative to the
+// scores m, or in the units of the logarithm base.
+//
+// One multiply-add takes a reference off the scores, as `base`, its product with scale
+// and log2 e.  That product's rounding is in every exponent (and in lse, which undoes
+// it), and leaves fp32 as a power of 2 from scores of 1e9 on.  So a CTA that ends with a
+// reference past kFarLog2 is walked again (kFar), with the references taken off the scores
+// themselves, base being 0: a score equal to its reference has the weight 1 at any size.
+// Always so would take 600 us for the 100 x 100 grid instead of 579, with a branch in
+// this walk 642.
+template <int HP, bool kBias, bool kGroups, bool kExact, bool kFar>
+__device__ __forceinline__ void walk(ForwardSmem<HP>& sm, const Inputs& in,
+                                     const uint32_t (&qf)[HP][8], const float2 (&p)[2],
+                                     const float (&tau)[HP][2], int g0, int g1, int b, int h,
+                                     int qt, int begin, int last, float (&o)[HP][4][4],
+                                     float (&m)[HP][2], float (&base)[HP][2], float2 (&l)[HP][2])
 {
-    extern __shared__ __align__(128) unsigned char smem[];
-    ForwardSmem<HP>& sm = *reinterpret_cast<ForwardSmem<HP>*>(smem);
-    const Inputs& in = a.in;
-    const int split = blockIdx.x % a.splits;  // its place in the cluster
-    int id = blockIdx.x / a.splits;
-    const int qt = id % a.q_tiles;
-    id /= a.q_tiles;
-    const int hg = id % (in.H / HP), b = id / (in.H / HP);
-    const int h = hg * HP, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = lane >> 2, t = lane & 3;
-    const int row = qt * kRows + warp * 16 + g;  // and row + 8
-    const bool on0 = row < in.Nq, on1 = row + 8 < in.Nq;
-    const int64_t q0 = (int64_t)b * in.Nq + row;
-
-    uint32_t qf[HP][8];
-#pragma unroll
-    for (int hh = 0; hh < HP; ++hh)
-        load_rows(qf[hh], in.q + (int64_t)b * in.Nq * in.ldq + (h + hh) * kDim, in.ldq, row, on0,
-                  on1, t);
-    // Scores are kept in units of the products q . k, and tau in the same units:
-    // one multiply-add adds the bias, another takes the reference off and
-    // changes to the base-2 logarithm.
+    const int lane = threadIdx.x & 31, t = lane & 3;
     const float unit = in.scale * kLog2e;
-    float2 p[2] = {};
-    float tau[HP][2] = {};
-    if constexpr (kBias) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (!(half ? on1 : on0)) continue;
-            const float2 at = __ldg(in.qp + q0 + 8 * half);
-            p[half] = make_float2(-at.x, -at.y);
-#pragma unroll
-            for (int hh = 0; hh < HP; ++hh)
-                tau[hh][half] = -__ldg(in.tau + (q0 + 8 * half) * in.H + h + hh) / in.scale;
-        }
-    }
-    int g0 = 0, g1 = 0;
-    if constexpr (kGroups) {
-        g0 = on0 ? __ldg(in.qg + q0) : -1;
-        g1 = on1 ? __ldg(in.qg + q0 + 8) : -1;
-    }
     // The reference that is taken off stays the same until a score is 2^kSlack
     // times above it: weights up to 2^kSlack are as exact as weights up to 1, and
     // after the first tiles nothing has to be scaled again.
     constexpr float kSlack = 8.0f;
     const float slack = kSlack / unit;
-    float o[HP][4][4] = {}, m[HP][2], base[HP][2] = {};
-    float2 l[HP][2] = {};
 #pragma unroll
-    for (int hh = 0; hh < HP; ++hh) m[hh][0] = m[hh][1] = -INFINITY;
-
+    for (int hh = 0; hh < HP; ++hh) {
+        // (a padding query's reference is never passed, so that what it holds moves no
+        // other row's)
+        m[hh][0] = g0 < 0 ? INFINITY : -INFINITY;
+        m[hh][1] = g1 < 0 ? INFINITY : -INFINITY;
+        base[hh][0] = base[hh][1] = 0.0f;
+        l[hh][0] = l[hh][1] = both(0.0f);
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[hh][d][i] = 0.0f;
+    }
     const LaneAt lanes = lane_at(lane);
     const TileCopy<HP> copy(in.k + (int64_t)b * in.Nk * in.ldk + h * kDim, in.ldk,
                             in.v + (int64_t)b * in.Nk * in.ldv + h * kDim, in.ldv, in.Nk);
-    const int tiles = (in.Nk + kTile - 1) / kTile;
-    const int begin = split * a.split_tiles, last = min(tiles, begin + a.split_tiles);
     for (int first = begin; first < last;) {
         const Tiles<kGroups> set{sm.bits, first, last, in.Nk / kTile};
         first = set.end();
@@ -209,13 +190,21 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocks)
                     const float f =
                         m[hh][half] == -INFINITY ? 0.0f : exp2_approx((m[hh][half] - n) * unit);
                     m[hh][half] = n;
-                    base[hh][half] = n == -INFINITY ? 0.0f : n * unit;
+                    if constexpr (!kFar) base[hh][half] = n == -INFINITY ? 0.0f : n * unit;
                     l[hh][half] = __fmul2_rn(l[hh][half], both(f));
 #pragma unroll
                     for (int d = 0; d < 4; ++d) {
                         o[hh][d][2 * half] *= f;
                         o[hh][d][2 * half + 1] *= f;
                     }
+                }
+            }
+            if constexpr (kFar) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float off = m[hh][half] == -INFINITY ? 0.0f : -m[hh][half];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[j][half] = __fadd2_rn(s[j][half], both(off));
                 }
             }
         };
@@ -281,12 +270,83 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocks)
             stage = next;
         }
     }
+}
 
-    // split keys: a row's sums, and their reference and sum of weights
-    float* part = reinterpret_cast<float*>(smem);
-    float2* part_ml = reinterpret_cast<float2*>(part + HP * kRows * kPartRow);
+// Where a CTA leaves its sums for the others of its cluster: in the place of the tiles.
+template <int HP>
+__device__ __forceinline__ float* split_sums(ForwardSmem<HP>& sm)
+{
     static_assert(HP * kRows * (kPartRow + 2) * sizeof(float) <= sizeof(sm.k) + sizeof(sm.v), "");
-    if (a.splits > 1) __syncthreads();  // the tiles have been read
+    return reinterpret_cast<float*>(&sm);
+}
+
+// All of a CTA's work but the join.  Returns whether it has to be done again with kFar.
+template <int HP, bool kBias, bool kGroups, bool kExact, bool kFar>
+__device__ __forceinline__ bool attend(ForwardSmem<HP>& sm, const ForwardArgs& a)
+{
+    const Inputs& in = a.in;
+    const int split = blockIdx.x % a.splits;  // its place in the cluster
+    int id = blockIdx.x / a.splits;
+    const int qt = id % a.q_tiles;
+    id /= a.q_tiles;
+    const int hg = id % (in.H / HP), b = id / (in.H / HP);
+    const int h = hg * HP, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int row = qt * kRows + warp * 16 + g;  // and row + 8
+    const bool on0 = row < in.Nq, on1 = row + 8 < in.Nq;
+    const int64_t q0 = (int64_t)b * in.Nq + row;
+
+    uint32_t qf[HP][8];
+#pragma unroll
+    for (int hh = 0; hh < HP; ++hh)
+        load_rows(qf[hh], in.q + (int64_t)b * in.Nq * in.ldq + (h + hh) * kDim, in.ldq, row, on0,
+                  on1, t);
+    // Scores are kept in units of the products q . k, and tau in the same units:
+    // one multiply-add adds the bias, another takes the reference off and
+    // changes to the base-2 logarithm.
+    float2 p[2] = {};
+    float tau[HP][2] = {};
+    if constexpr (kBias) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (!(half ? on1 : on0)) continue;
+            const float2 at = __ldg(in.qp + q0 + 8 * half);
+            p[half] = make_float2(-at.x, -at.y);
+#pragma unroll
+            for (int hh = 0; hh < HP; ++hh)
+                tau[hh][half] =
+                    tau_units(__ldg(in.tau + (q0 + 8 * half) * in.H + h + hh), in.scale);
+        }
+    }
+    int g0 = 0, g1 = 0;
+    if constexpr (kGroups) {
+        g0 = on0 ? __ldg(in.qg + q0) : -1;
+        g1 = on1 ? __ldg(in.qg + q0 + 8) : -1;
+    }
+    const int tiles = (in.Nk + kTile - 1) / kTile;
+    const int begin = split * a.split_tiles, last = min(tiles, begin + a.split_tiles);
+    float o[HP][4][4], m[HP][2], base[HP][2];
+    float2 l[HP][2];
+    walk<HP, kBias, kGroups, kExact, kFar>(sm, in, qf, p, tau, g0, g1, b, h, qt, begin, last, o, m,
+                                           base, l);
+    // References on the way to the last one leave nothing behind where they were far, their
+    // sums being scaled by 0, unless these had left fp32.
+    bool far = false;
+#pragma unroll
+    for (int hh = 0; hh < HP; ++hh) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+            far = far || ((half ? g1 : g0) >= 0 &&
+                          (is_far(base[hh][half]) ||
+                           !(l[hh][half].x + l[hh][half].y < INFINITY)));
+    }
+    far = __syncthreads_or(far);  // (and the tiles have been read)
+    if (!kFar && far) return true;
+
+    // split keys: a row's sums, and their reference and sum of weights (of a far walk the
+    // reference as a score, told by the sum's sign)
+    float* part = split_sums(sm);
+    float2* part_ml = reinterpret_cast<float2*>(part + HP * kRows * kPartRow);
 #pragma unroll
     for (int hh = 0; hh < HP; ++hh) {
 #pragma unroll
@@ -304,8 +364,9 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocks)
                 for (int d = 0; d < 4; ++d)
                     dst[4 * d + t] = make_float2(o[hh][d][2 * half], o[hh][d][2 * half + 1]);
                 if (t == 0)
-                    part_ml[r] = dead ? make_float2(-INFINITY, 0.0f)
-                                      : make_float2(base[hh][half], sum);
+                    part_ml[r] = dead   ? make_float2(-INFINITY, 0.0f)
+                                 : kFar ? make_float2(m[hh][half], -sum)
+                                        : make_float2(base[hh][half], sum);
                 continue;
             }
             if (!(half ? on1 : on0)) continue;
@@ -318,39 +379,89 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocks)
                     dead ? 0u : pack_bf16(o[hh][d][2 * half] * w, o[hh][d][2 * half + 1] * w);
             if (a.lse != nullptr && t == 0)
                 a.lse[((int64_t)b * in.H + h + hh) * in.Nq + q] =
-                    dead ? -INFINITY : (base[hh][half] + log2f(sum)) * kLn2;
+                    dead   ? -INFINITY
+                    : kFar ? far_lse(m[hh][half], in.scale, sum)
+                           : (base[hh][half] + log2f(sum)) * kLn2;
         }
     }
-    if (a.splits == 1) return;
-    // Each CTA joins every splits-th 16 rows, eight lanes and four channels a row.
-    cluster_sync();
+    return false;
+}
+
+// The parts of up to kMost CTAs of a cluster: each CTA joins every splits-th 16 rows,
+// eight lanes and four channels a row.
+template <int HP, int kMost>
+__device__ __forceinline__ void join_splits(ForwardSmem<HP>& sm, const ForwardArgs& a)
+{
+    const Inputs& in = a.in;
+    const int split = blockIdx.x % a.splits;
+    int id = blockIdx.x / a.splits;
+    const int qt = id % a.q_tiles;
+    id /= a.q_tiles;
+    const int h = id % (in.H / HP) * HP, b = id / (in.H / HP);
+    const float unit = in.scale * kLog2e;
+    const float* part = split_sums(sm);
+    const float2* part_ml = reinterpret_cast<const float2*>(part + HP * kRows * kPartRow);
     const int c = threadIdx.x & 7;
     for (int r = split * 16 + (int)(threadIdx.x >> 3); r < HP * kRows; r += 16 * a.splits) {
         const int q = qt * kRows + r % kRows, hh = h + r / kRows;
         if (q >= in.Nq) continue;
         const uint32_t at = smem_addr(part + r * kPartRow + 4 * c), at_ml = smem_addr(part_ml + r);
+        // (all at once: one of these reads takes as long as all of them)
+        float2 ml[kMost];
+        float4 v[kMost];
+#pragma unroll
+        for (int s = 0; s < kMost; ++s) {
+            ml[s] = make_float2(-INFINITY, 0.0f);
+            if (s < a.splits) {
+                ml[s] = remote_f32x2(remote_addr(at_ml, s));
+                v[s] = remote_f32x4(remote_addr(at, s));
+            }
+        }
+        bool far_row = false;  // of a CTA: then all references as scores
+#pragma unroll
+        for (int s = 0; s < kMost; ++s) far_row = far_row || ml[s].y < 0.0f;
         float m = -INFINITY;
-        for (int s = 0; s < a.splits; ++s) m = fmaxf(m, remote_f32x2(remote_addr(at_ml, s)).x);
+#pragma unroll
+        for (int s = 0; s < kMost; ++s) {
+            if (far_row && ml[s].y > 0.0f) ml[s].x /= unit;
+            m = fmaxf(m, ml[s].x);
+        }
         float sum = 0.0f;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int s = 0; s < a.splits; ++s) {
-            const float2 ml = remote_f32x2(remote_addr(at_ml, s));
-            const float4 v = remote_f32x4(remote_addr(at, s));
-            if (ml.y == 0.0f) continue;  // nothing seen: the sums may be those of a padding row
-            const float w = exp2_approx(ml.x - m);
-            sum = fmaf(w, ml.y, sum);
-            acc.x = fmaf(w, v.x, acc.x);
-            acc.y = fmaf(w, v.y, acc.y);
-            acc.z = fmaf(w, v.z, acc.z);
-            acc.w = fmaf(w, v.w, acc.w);
+#pragma unroll
+        for (int s = 0; s < kMost; ++s) {
+            // nothing seen: the sums may be those of a padding row
+            if (s >= a.splits || ml[s].y == 0.0f) continue;
+            const float w = exp2_approx(far_row ? (ml[s].x - m) * unit : ml[s].x - m);
+            sum = fmaf(w, fabsf(ml[s].y), sum);
+            acc.x = fmaf(w, v[s].x, acc.x);
+            acc.y = fmaf(w, v[s].y, acc.y);
+            acc.z = fmaf(w, v[s].z, acc.z);
+            acc.w = fmaf(w, v[s].w, acc.w);
         }
         const float w = sum == 0.0f ? 0.0f : 1.0f / sum;
         *reinterpret_cast<uint2*>(a.out + (((int64_t)b * in.Nq + q) * in.H + hh) * kDim + c * 4) =
             make_uint2(pack_bf16(acc.x * w, acc.y * w), pack_bf16(acc.z * w, acc.w * w));
         if (a.lse != nullptr && c == 0)
             a.lse[((int64_t)b * in.H + hh) * in.Nq + q] =
-                sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
+                sum == 0.0f ? -INFINITY
+                : far_row   ? far_lse(m, in.scale, sum)
+                            : (m + log2f(sum)) * kLn2;
     }
+}
+
+template <int HP, bool kBias, bool kGroups, bool kExact>
+__global__ void __launch_bounds__(kAttnThreads, kBlocks)
+    attention_forward_kernel(const __grid_constant__ ForwardArgs a)
+{
+    extern __shared__ __align__(128) unsigned char smem[];
+    ForwardSmem<HP>& sm = *reinterpret_cast<ForwardSmem<HP>*>(smem);
+    if (attend<HP, kBias, kGroups, kExact, false>(sm, a))
+        attend<HP, kBias, kGroups, kExact, true>(sm, a);
+    if (a.splits == 1) return;
+    cluster_sync();
+    if (a.splits <= kMaxSplits / 2) join_splits<HP, kMaxSplits / 2>(sm, a);
+    else join_splits<HP, kMaxSplits>(sm, a);
     cluster_sync();  // nobody's shared memory goes while others read it
 }
 

@@ -418,6 +418,32 @@ __device__ __forceinline__ bool sees(int q_group, int k_group)
     return q_group >= 0 && k_group >= 0 && (k_group == 0 || k_group == q_group);
 }
 
+// Rows whose scores are far from zero: the logarithm of a weight is a score minus a
+// reference, each times scale and log2 e; taken as one multiply-add it keeps the
+// rounding of the reference's product, 2^-12 at kFarLog2 and without bound beyond.  Far
+// rows take the reference off first.  (A row that sees nothing has -infinity here.)
+constexpr float kFarLog2 = 4096.0f;
+__device__ __forceinline__ bool is_far(float reference_log2)
+{
+    return fabsf(reference_log2) > kFarLog2 && fabsf(reference_log2) != INFINITY;
+}
+
+// tau, negated and in units of q . k
+__device__ __forceinline__ float tau_units(float tau, float scale) { return -tau / scale; }
+
+// A far row's lse, from its reference (a score in units of q . k) and the sum of its
+// weights, and the logarithm of one of its weights from lse.  Neither is contracted, so
+// that where the sum is 1 the key that lse comes from has the weight 1 at any size.
+__device__ __forceinline__ float far_lse(float reference, float scale, float sum)
+{
+    return __fadd_rn(__fmul_rn(reference, scale), log2f(sum) * kLn2);
+}
+
+__device__ __forceinline__ float far_log2(float score, float scale, float lse)
+{
+    return __fmul_rn(__fsub_rn(__fmul_rn(score, scale), lse), kLog2e);
+}
+
 // Distances of a row's point (given negated, nx and ny) from two points.
 __device__ __forceinline__ float2 distances(float nx, float ny, float2 x, float2 y)
 {
@@ -428,7 +454,8 @@ __device__ __forceinline__ float2 distances(float nx, float ny, float2 x, float2
 
 // The points of a tile, x and y apart so that two neighbours load as a pair.
 struct Points {
-    float x[kTile], y[kTile];
+    alignas(8) float x[kTile];
+    alignas(8) float y[kTile];
 };
 
 // The points and groups of the tile's rows r0 .. r0 + 63 of an item.

@@ -42,11 +42,12 @@ template <int HP>
 struct BackwardSmem {
     alignas(128) unsigned char a[2][HP * kTileBytes];  // keys, or queries
     alignas(128) unsigned char b[2][HP * kTileBytes];  // values, or the output's gradient
-    float rows[2][HP][3][kTile];  // of the queries (keys' kernel): lse, tau, D
+    alignas(8) float rows[2][HP][3][kTile];  // of the queries (keys' kernel): lse, tau, D
     float dots[HP][kTile];        // D's sums where the keys are split
     Points pos[2];
     int32_t group[2][kTile];
     TileBits bits;
+    int32_t far;                  // a query is far (keys' kernel)
 };
 
 template <int HP, bool kBias, bool kGroups>
@@ -155,10 +156,66 @@ __device__ __forceinline__ float quad_sum(float x)
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
+// The logarithms of the weights of a warp's 16 queries, `row` the thread's first, from
+// their products, where a query of theirs is far.
+template <bool kBias>
+__device__ __forceinline__ void far_rows(float2 (&s)[4][2], const float2 (&dist)[4][2],
+                                         const BackwardArgs& a, const float (&e)[2], int b, int h,
+                                         int row)
+{
+    const Inputs& in = a.in;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const bool live = e[half] != -INFINITY;
+        const int64_t q = (int64_t)row + 8 * half;
+        const float lse = live ? __ldg(a.lse + ((int64_t)b * in.H + h) * in.Nq + q) : INFINITY;
+        float tau = 0.0f;
+        if (kBias && live)
+            tau = tau_units(__ldg(in.tau + ((int64_t)b * in.Nq + q) * in.H + h), in.scale);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (kBias) s[j][half] = __ffma2_rn(dist[j][half], both(tau), s[j][half]);
+            s[j][half] = make_float2(far_log2(s[j][half].x, in.scale, lse),
+                                     far_log2(s[j][half].y, in.scale, lse));
+        }
+    }
+}
+
+// The same with the queries as columns, step st of a tile; `e` the tile's.
+template <bool kBias>
+__device__ __forceinline__ void far_columns(float2 (&s)[4][2], const float2 (&dist)[4][2],
+                                            const BackwardArgs& a, const float* e, int b, int h,
+                                            int tile, int st)
+{
+    const Inputs& in = a.in;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int at = kHalf * st + 8 * j + 2 * (threadIdx.x & 3) + c;
+            const int64_t q = (int64_t)tile * kTile + at;
+            const bool live = q < in.Nq && e[at] != -INFINITY;
+            const float lse = live ? __ldg(a.lse + ((int64_t)b * in.H + h) * in.Nq + q) : INFINITY;
+            float tau = 0.0f;
+            if (kBias && live)
+                tau = tau_units(__ldg(in.tau + ((int64_t)b * in.Nq + q) * in.H + h), in.scale);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float& x = c ? s[j][half].y : s[j][half].x;
+                if constexpr (kBias) x = fmaf(c ? dist[j][half].y : dist[j][half].x, tau, x);
+                x = far_log2(x, in.scale, lse);
+            }
+        }
+    }
+}
+
 // 64 queries and the tiles [begin, last) of the keys: D (and what the last
 // kernel needs of the queries beside it), or with kGrad, given D, dq and dtau.
-template <int HP, bool kBias, bool kGroups, bool kGrad, bool kExact>
-__device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardArgs& a, int id,
+// Returns whether a query of theirs is far, and they have to be walked again with kFar:
+// a walk of its own, since a branch in this one takes registers that it has not got (7 %
+// of the gradient of 5000 queries).
+template <int HP, bool kBias, bool kGroups, bool kGrad, bool kExact, bool kFar>
+__device__ __forceinline__ bool walk_keys(BackwardSmem<HP>& sm, const BackwardArgs& a, int id,
                                           int split)
 {
     const Inputs& in = a.in;
@@ -286,13 +343,17 @@ __device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardAr
                     float2 s[4][2], dp[4][2];
                     products(s, qf[hh], sk, st, lanes);
                     products(dp, of[hh], sv, st, lanes);
+                    if constexpr (kFar) far_rows<kBias>(s, dist, a, e[hh], b, h + hh, row);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
-                            float2 x = __ffma2_rn(s[j][half], both(scale), both(e[hh][half]));
-                            if constexpr (kBias)
-                                x = __ffma2_rn(dist[j][half], both(tau[hh][half]), x);
+                            float2 x = s[j][half];
+                            if constexpr (!kFar) {
+                                x = __ffma2_rn(x, both(scale), both(e[hh][half]));
+                                if constexpr (kBias)
+                                    x = __ffma2_rn(dist[j][half], both(tau[hh][half]), x);
+                            }
                             if (!clear) mask(x, hide >> (4 * j + 2 * half), -INFINITY);
                             s[j][half] = make_float2(exp2_approx(x.x), exp2_approx(x.y));
                         }
@@ -370,11 +431,16 @@ __device__ __forceinline__ void walk_keys(BackwardSmem<HP>& sm, const BackwardAr
             }
         }
     }
+    bool far = false;
+#pragma unroll
+    for (int hh = 0; hh < HP; ++hh) far = far || is_far(e[hh][0]) || is_far(e[hh][1]);
+    return !kFar && __syncthreads_or(far);
 }
 
-// 64 keys and all queries: dk and dv.
-template <int HP, bool kBias, bool kGroups, bool kExact>
-__device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const BackwardArgs& a, int id)
+// 64 keys and all queries: dk and dv.  Returns whether a query that was read is far, and
+// they have to be walked again with kFar.
+template <int HP, bool kBias, bool kGroups, bool kExact, bool kFar>
+__device__ __forceinline__ bool walk_queries(BackwardSmem<HP>& sm, const BackwardArgs& a, int id)
 {
     const Inputs& in = a.in;
     const int kt = id % a.k_tiles;
@@ -409,6 +475,9 @@ __device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const Backwar
     }
     const float scale = in.scale * kLog2e;
     float dk[HP][4][4] = {}, dv[HP][4][4] = {};
+    // (a barrier comes before the first tile; kFar writes nothing, since others may still be
+    // reading it)
+    if (!kFar && threadIdx.x == 0) sm.far = 0;
 
     const LaneAt lanes = lane_at(lane);
     const TileCopy<HP> copy(in.q + (int64_t)b * in.Nq * in.ldq + h * kDim, in.ldq,
@@ -435,6 +504,11 @@ __device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const Backwar
                 cp_wait<0>();
             }
             __syncthreads();
+            if (!kFar && (int)threadIdx.x < kTile) {
+#pragma unroll
+                for (int hh = 0; hh < HP; ++hh)
+                    if (is_far(sm.rows[stage][hh][0][threadIdx.x])) sm.far = 1;
+            }
             const bool clear = set.clear(tile);
 #pragma unroll
             for (int st = 0; st < kTile / kHalf; ++st) {
@@ -470,6 +544,8 @@ __device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const Backwar
                     float2 s[4][2], dp[4][2];
                     products(s, kf[hh], sq, st, lanes);
                     products(dp, vf[hh], so, st, lanes);
+                    if constexpr (kFar)
+                        far_columns<kBias>(s, dist, a, sm.rows[stage][hh][0], b, h + hh, tile, st);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int at = kHalf * st + 8 * j + 2 * t;
@@ -479,8 +555,11 @@ __device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const Backwar
                             r[k] = *reinterpret_cast<const float2*>(&sm.rows[stage][hh][k][at]);
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
-                            float2 x = __ffma2_rn(s[j][half], both(scale), r[0]);
-                            if constexpr (kBias) x = __ffma2_rn(dist[j][half], r[1], x);
+                            float2 x = s[j][half];
+                            if constexpr (!kFar) {
+                                x = __ffma2_rn(x, both(scale), r[0]);
+                                if constexpr (kBias) x = __ffma2_rn(dist[j][half], r[1], x);
+                            }
                             if (!clear) mask(x, hide >> (4 * j + 2 * half), -INFINITY);
                             s[j][half] = make_float2(exp2_approx(x.x), exp2_approx(x.y));
                             dp[j][half] = __fmul2_rn(
@@ -504,23 +583,47 @@ __device__ __forceinline__ void walk_queries(BackwardSmem<HP>& sm, const Backwar
         store_rows(a.dk, k0, in.H, h + hh, dk[hh], in.scale, on0, on1, t);
         store_rows(a.dv, k0, in.H, h + hh, dv[hh], 1.0f, on0, on1, t);
     }
+    __syncthreads();
+    return !kFar && sm.far;
+}
+
+// (not inlined: the registers are for the walks that are taken)
+template <int HP, bool kBias, bool kGroups, bool kGrad, bool kExact>
+__device__ __noinline__ void far_keys(BackwardSmem<HP>& sm, const BackwardArgs& a, int id, int split)
+{
+    walk_keys<HP, kBias, kGroups, kGrad, kExact, true>(sm, a, id, split);
+}
+
+template <int HP, bool kBias, bool kGroups, bool kExact>
+__device__ __noinline__ void far_queries(BackwardSmem<HP>& sm, const BackwardArgs& a, int id)
+{
+    walk_queries<HP, kBias, kGroups, kExact, true>(sm, a, id);
 }
 
 template <int HP, bool kBias, bool kGroups>
-__global__ void __launch_bounds__(kAttnThreads, kDotBlocks) attention_dots_kernel(const BackwardArgs a)
+__global__ void __launch_bounds__(kAttnThreads, kDotBlocks)
+    attention_dots_kernel(const __grid_constant__ BackwardArgs a)
 {
     __shared__ BackwardSmem<HP> sm;
-    const int id = blockIdx.x / a.splits;
-    walk_keys<HP, kBias, kGroups, false, false>(sm, a, id, blockIdx.x - id * a.splits);
+    const int id = blockIdx.x / a.splits, split = blockIdx.x - id * a.splits;
+    if (walk_keys<HP, kBias, kGroups, false, false, false>(sm, a, id, split))
+        far_keys<HP, kBias, kGroups, false, false>(sm, a, id, split);
 }
 
 template <bool kBias, bool kGroups, bool kExact>
-__global__ void __launch_bounds__(kAttnThreads, kBlocks) attention_grad_kernel(const BackwardArgs a)
+__global__ void __launch_bounds__(kAttnThreads, kBlocks)
+    attention_grad_kernel(const __grid_constant__ BackwardArgs a)
 {
     __shared__ BackwardSmem<1> sm;
     const int keys = a.k_tiles * a.in.H * a.in.B;  // the longer ones first
-    if ((int)blockIdx.x < keys) walk_queries<1, kBias, kGroups, kExact>(sm, a, blockIdx.x);
-    else walk_keys<1, kBias, kGroups, true, kExact>(sm, a, blockIdx.x - keys, 0);
+    const int id = blockIdx.x;
+    if (id < keys) {
+        if (walk_queries<1, kBias, kGroups, kExact, false>(sm, a, id))
+            far_queries<1, kBias, kGroups, kExact>(sm, a, id);
+    } else {
+        if (walk_keys<1, kBias, kGroups, true, kExact, false>(sm, a, id - keys, 0))
+            far_keys<1, kBias, kGroups, true, kExact>(sm, a, id - keys, 0);
+    }
 }
 
 template <bool kGroups>
