@@ -677,9 +677,8 @@ msda_status_t msda_query_attention(const msda_attention_t* p, void* out, float* 
  *   grad_out [B, Nq, H * 32] bf16
  *   grad_q [B, Nq, H, 32], grad_k and grad_v [B, Nk, H, 32] bf16, contiguous,
  *   written; grad_tau [B, Nq, H] fp32, written (NULL where p->tau is)
- * lse is fp32, so p is off by some 2^-23 |lse| of itself; the key that lse comes
- * from keeps its weight at any size, but among scores past 1e7 a row's other
- * weights are lost in lse's rounding.
+ * lse is fp32, so p is off by some 2^-23 |lse| of itself; from |lse| = 2839 on a
+ * row's weights are divided by their sum, so that they stay weights at any size.
  * p and ds are rounded to bf16 for the products with grad_out, k and q (to 16
  * bits for up to 1024 rows times heads times items on one side); the
  * sum over j of p dp is formed in fp32 from the unrounded values.  Alignment

@@ -34,7 +34,9 @@ struct BackwardArgs {
     const float* lse;
     __nv_bfloat16 *dq, *dk, *dv;
     float* dtau;
-    float* rows;  // [3, B, H, Nq]: -lse and -tau in units of log 2, D
+    // [3, B, H, Nq]: -lse and -tau in units of log 2 (of a far query the logarithm of its
+    // weights' sum, negated, in the place of tau), D
+    float* rows;
     int q_tiles, k_tiles, splits, split_tiles;
 };
 
@@ -43,7 +45,8 @@ struct BackwardSmem {
     alignas(128) unsigned char a[2][HP * kTileBytes];  // keys, or queries
     alignas(128) unsigned char b[2][HP * kTileBytes];  // values, or the output's gradient
     alignas(8) float rows[2][HP][3][kTile];  // of the queries (keys' kernel): lse, tau, D
-    float dots[HP][kTile];        // D's sums where the keys are split
+    float dots[HP][kTile];        // D's sums where the keys are split,
+    float weights[HP][kTile];     // and those of the weights in a far walk
     Points pos[2];
     int32_t group[2][kTile];
     TileBits bits;
@@ -156,9 +159,19 @@ __device__ __forceinline__ float quad_sum(float x)
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
+// D of a far query from its sums, and what its weights' logarithms are moved by.
+__device__ __forceinline__ float normalise(float& norm, float dot, float weights)
+{
+    if (!(weights > 0.0f && weights < INFINITY)) return norm = 0.0f, dot;  // (lse is another's)
+    norm = -log2f(weights);
+    return dot / weights;
+}
+
 // The logarithms of the weights of a warp's 16 queries, `row` the thread's first, from
-// their products, where a query of theirs is far.
-template <bool kBias>
+// their products, where a query of theirs is far.  Past 2^24 lse holds nothing of the
+// logarithm of the weights' sum (where keys tie), so with kNormed a far query's weights
+// are divided by their sum, which the walk for D has found.
+template <bool kBias, bool kNormed>
 __device__ __forceinline__ void far_rows(float2 (&s)[4][2], const float2 (&dist)[4][2],
                                          const BackwardArgs& a, const float (&e)[2], int b, int h,
                                          int row)
@@ -172,20 +185,23 @@ __device__ __forceinline__ void far_rows(float2 (&s)[4][2], const float2 (&dist)
         float tau = 0.0f;
         if (kBias && live)
             tau = tau_units(__ldg(in.tau + ((int64_t)b * in.Nq + q) * in.H + h), in.scale);
+        float norm = 0.0f;
+        if (kNormed && is_far(e[half]))
+            norm = a.rows[((int64_t)in.B * in.H + (int64_t)b * in.H + h) * in.Nq + q];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if constexpr (kBias) s[j][half] = __ffma2_rn(dist[j][half], both(tau), s[j][half]);
-            s[j][half] = make_float2(far_log2(s[j][half].x, in.scale, lse),
-                                     far_log2(s[j][half].y, in.scale, lse));
+            s[j][half] = make_float2(far_log2(s[j][half].x, in.scale, lse) + norm,
+                                     far_log2(s[j][half].y, in.scale, lse) + norm);
         }
     }
 }
 
-// The same with the queries as columns, step st of a tile; `e` the tile's.
+// The same with the queries as columns, step st of a tile; `e` and `norms` the tile's.
 template <bool kBias>
 __device__ __forceinline__ void far_columns(float2 (&s)[4][2], const float2 (&dist)[4][2],
-                                            const BackwardArgs& a, const float* e, int b, int h,
-                                            int tile, int st)
+                                            const BackwardArgs& a, const float* e,
+                                            const float* norms, int b, int h, int tile, int st)
 {
     const Inputs& in = a.in;
 #pragma unroll
@@ -203,7 +219,7 @@ __device__ __forceinline__ void far_columns(float2 (&s)[4][2], const float2 (&di
             for (int half = 0; half < 2; ++half) {
                 float& x = c ? s[j][half].y : s[j][half].x;
                 if constexpr (kBias) x = fmaf(c ? dist[j][half].y : dist[j][half].x, tau, x);
-                x = far_log2(x, in.scale, lse);
+                x = far_log2(x, in.scale, lse) + (is_far(e[at]) ? norms[at] : 0.0f);
             }
         }
     }
@@ -265,6 +281,7 @@ __device__ __forceinline__ bool walk_keys(BackwardSmem<HP>& sm, const BackwardAr
     }
     const float scale = in.scale * kLog2e;
     float D[HP][2] = {}, dt[HP][2] = {}, dq[HP][4][4] = {};
+    float weights[HP][2] = {};  // their sums, of the far walk for D
     const int64_t plane = (int64_t)in.B * in.H * in.Nq;
     if constexpr (kGrad) {
 #pragma unroll
@@ -343,7 +360,8 @@ __device__ __forceinline__ bool walk_keys(BackwardSmem<HP>& sm, const BackwardAr
                     float2 s[4][2], dp[4][2];
                     products(s, qf[hh], sk, st, lanes);
                     products(dp, of[hh], sv, st, lanes);
-                    if constexpr (kFar) far_rows<kBias>(s, dist, a, e[hh], b, h + hh, row);
+                    if constexpr (kFar)
+                        far_rows<kBias, kGrad>(s, dist, a, e[hh], b, h + hh, row);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -367,6 +385,13 @@ __device__ __forceinline__ bool walk_keys(BackwardSmem<HP>& sm, const BackwardAr
                                 sum[half] = __ffma2_rn(s[j][half], dp[j][half], sum[half]);
                         D[hh][0] += sum[0].x + sum[0].y;
                         D[hh][1] += sum[1].x + sum[1].y;
+                        if constexpr (kFar) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                for (int half = 0; half < 2; ++half)
+                                    weights[hh][half] += s[j][half].x + s[j][half].y;
+                        }
                     } else {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -396,13 +421,21 @@ __device__ __forceinline__ bool walk_keys(BackwardSmem<HP>& sm, const BackwardAr
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 D[hh][half] = quad_sum(D[hh][half]);
+                if constexpr (kFar) weights[hh][half] = quad_sum(weights[hh][half]);
                 if (t != 0) continue;
-                if (a.splits > 1) sm.dots[hh][warp * 16 + g + 8 * half] = D[hh][half];
+                if (a.splits > 1) {
+                    sm.dots[hh][warp * 16 + g + 8 * half] = D[hh][half];
+                    if constexpr (kFar) sm.weights[hh][warp * 16 + g + 8 * half] = weights[hh][half];
+                }
                 if (split != 0 || !(half ? on1 : on0)) continue;
                 const int64_t i = ((int64_t)b * in.H + h + hh) * in.Nq + row + 8 * half;
                 a.rows[i] = e[hh][half];
                 a.rows[plane + i] = tau[hh][half];
-                if (a.splits == 1) a.rows[2 * plane + i] = D[hh][half];
+                if (a.splits == 1) {
+                    if (kFar && is_far(e[hh][half]))
+                        D[hh][half] = normalise(a.rows[plane + i], D[hh][half], weights[hh][half]);
+                    a.rows[2 * plane + i] = D[hh][half];
+                }
             }
         }
         if (a.splits > 1) {
@@ -413,7 +446,14 @@ __device__ __forceinline__ bool walk_keys(BackwardSmem<HP>& sm, const BackwardAr
                 float sum = 0.0f;
                 for (int s = 0; s < a.splits; ++s)
                     sum += remote_f32(remote_addr(smem_addr(&sm.dots[0][i]), s));
-                a.rows[2 * plane + ((int64_t)b * in.H + h + i / kTile) * in.Nq + q] = sum;
+                const int64_t at = ((int64_t)b * in.H + h + i / kTile) * in.Nq + q;
+                if constexpr (kFar) {
+                    float all = 0.0f;
+                    for (int s = 0; s < a.splits; ++s)
+                        all += remote_f32(remote_addr(smem_addr(&sm.weights[0][i]), s));
+                    if (is_far(a.rows[at])) sum = normalise(a.rows[plane + at], sum, all);
+                }
+                a.rows[2 * plane + at] = sum;
             }
             cluster_sync();  // nobody's shared memory goes while others read it
         }
@@ -545,7 +585,8 @@ __device__ __forceinline__ bool walk_queries(BackwardSmem<HP>& sm, const Backwar
                     products(s, kf[hh], sq, st, lanes);
                     products(dp, vf[hh], so, st, lanes);
                     if constexpr (kFar)
-                        far_columns<kBias>(s, dist, a, sm.rows[stage][hh][0], b, h + hh, tile, st);
+                        far_columns<kBias>(s, dist, a, sm.rows[stage][hh][0],
+                                           sm.rows[stage][hh][1], b, h + hh, tile, st);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int at = kHalf * st + 8 * j + 2 * t;

@@ -73,6 +73,46 @@ def test_a_tau_that_cuts_off_all_but_the_nearest(size, tau, groups):
     assert bool(((gv.double() - sums[0]).abs() <= 2.0 ** -16 * sums[1] + 2.0 ** -8 * sums[0].abs()).all())
 
 
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("tau", [3e7, 1e10, 1e20])
+@pytest.mark.parametrize("groups", [False, True])
+def test_two_keys_at_the_same_distance(size, tau, groups):
+    """Half-way between two keys, with q = 0: the weights are a half each, although lse has no
+    room for the logarithm of 2.  Tolerances: a half is exact, also in bf16; D and dp as above,
+    so ds is off by 2^-17 a, a = sum over both of |do v|, beside what bf16 leaves over (h |ds|)."""
+    B, Nq, Nk, H = size
+    a, near = line(*size, tau, groups, 70 + sum(size))
+    near = near % (Nk - 1)
+    a["q_points"][..., 0] = near + 0.5
+    a["q"].zero_()
+    on = torch.ones(B, Nq, 1, 1, device="cuda", dtype=torch.float64)
+    if groups:
+        on[:, -1] = 0
+    out, lse = msda.msda_query_attention(**a)
+    at = [(near + i)[:, :, None, None].expand(B, Nq, H, 32) for i in (0, 1)]
+    k, v = ([torch.gather(a[n].double(), 1, i) for i in at] for n in ("k", "v"))
+    want = (v[0] + v[1]) / 2 * on
+    got = out.double().view(B, Nq, H, 32)
+    assert bool(((got - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -22 * (v[0].abs() + v[1].abs())).all())
+    do = torch.randn(B, Nq, H * 32, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5)).bfloat16()
+    gq, gk, gv, gt = msda.msda_query_attention_backward(**a, lse=lse, grad_out=do)
+    d = do.double().view(B, Nq, H, 32) * on
+    dp = [(d * t).sum(-1, keepdim=True) for t in v]
+    ds = (dp[0] - dp[1]) / 4                     # of the first; the second's is its negative
+    off = 2.0 ** -17 * sum((d * t).abs().sum(-1, keepdim=True) for t in v)
+    scale = 32 ** -0.5
+    want = scale * ds * (k[0] - k[1])
+    tol = scale * (off + 2.0 ** -8 * ds.abs()) * (k[0].abs() + k[1].abs()) + 2.0 ** -8 * want.abs()
+    assert bool(((gq.double() - want).abs() <= tol).all())
+    assert bool((gk == 0).all())
+    assert bool((gt.double().abs() <= off[..., 0] + 2.0 ** -20 * ds.abs()[..., 0]).all())
+    sums = torch.zeros(2, B, Nk, H, 32, device="cuda", dtype=torch.float64)
+    for i in at:
+        sums[0].scatter_add_(1, i, d / 2)
+        sums[1].scatter_add_(1, i, d.abs() / 2)
+    assert bool(((gv.double() - sums[0]).abs() <= 2.0 ** -16 * sums[1] + 2.0 ** -8 * sums[0].abs()).all())
+
+
 @pytest.mark.parametrize("size", [(1, 300, 301, 8), (2, 1, 4097, 2), (1, 70, 129, 1), (4, 2400, 75, 8)])
 @pytest.mark.parametrize("groups", [None, "shared"])
 @pytest.mark.parametrize("shift", [300.0, 3000.0, 30000.0])
