@@ -320,10 +320,13 @@ msda_status_t run_clip(const msda_grad_t* tensors, int count, float max_norm, fl
                        float scale, double* partial, float* total_norm, cudaStream_t s)
 {
     ClipTable<N> t;  // at most 31 KB of stack
-    int partials = 0;
-    for (int at = 0; at == 0 || at < count; at += N) {
+    // (the first part is filled last, and first to be launched)
+    for (int at = (count - 1) / N * N; at >= 0; at -= N)
         if (!fill_table(t, tensors + at, std::min(N, count - at)))
             return api_fail(MSDA_ERR_UNSUPPORTED, "the tensors hold too many values");
+    int partials = 0;
+    for (int at = 0; at == 0 || at < count; at += N) {
+        if (at > 0) fill_table(t, tensors + at, std::min(N, count - at));
         const int grid = clip_grid(t.tiles);
         clip_squares_kernel<N><<<grid, kClipThreads, 0, s>>>(t, partial + partials);
         partials += grid;
