@@ -766,12 +766,16 @@ def sca_backward_inputs(spatial_shapes, level_start_index, attention_logits, pos
 
 def _same_dense_layout(a, b):
     """Whether a and b hold one value per element in the same order, without gaps."""
-    torch = _torch()
-    formats = [torch.contiguous_format] + {4: [torch.channels_last],
-                                           5: [torch.channels_last_3d]}.get(a.dim(), [])
-    # (not by the strides: those of dimensions of size 1 say nothing)
-    return any(a.is_contiguous(memory_format=f) and b.is_contiguous(memory_format=f)
-               for f in formats)
+    if 0 in a.shape:
+        return True
+    # (of a dimension of size 1 the stride says nothing)
+    order = sorted((sa, n, sb) for n, sa, sb in zip(a.shape, a.stride(), b.stride()) if n != 1)
+    at = 1
+    for sa, n, sb in order:
+        if sa != at or sb != at:
+            return False
+        at *= n
+    return True
 
 
 def msda_clip_grad_norm(grads, max_norm, eps=1e-6, grad_scale=1.0, out=None, total_norm=None,
@@ -779,8 +783,8 @@ def msda_clip_grad_norm(grads, max_norm, eps=1e-6, grad_scale=1.0, out=None, tot
     """The gradients (a list of fp32 or bf16 tensors) scaled by grad_scale and
     clipped to the global norm max_norm, in place or into `out` (a list of the
     same shapes, fp32 or bf16) -> total_norm [1] fp32, the norm before the
-    clipping.  Tensors are contiguous, or
-    channels-last together with their outputs."""
+    clipping.  Tensors hold their values without gaps, in any order of their
+    dimensions that their outputs share."""
     torch = _torch()
     grads = list(grads)
     n = len(grads)
