@@ -798,7 +798,12 @@ def msda_clip_grad_norm(grads, max_norm, eps=1e-6, grad_scale=1.0, out=None, tot
     every = grads if out is None else grads + outs
     Tensor, dtype_of = torch.Tensor, operator.attrgetter("dtype")
     first = every[0] if n else total_norm
-    if first.get_device() < 0 or len(set(map(Tensor.get_device, every))) > 1:
+    try:
+        devices = set(map(Tensor.get_device, every or [first]))
+    except TypeError:
+        raise MsdaError("msda_clip_grad_norm: the list holds something that is no tensor (the "
+                        "gradient of a parameter that has none?)") from None
+    if len(devices) > 1 or devices.pop() < 0:
         raise MsdaError("msda_clip_grad_norm: the tensors must be on one CUDA device")
     codes = {torch.float32: MSDA_F32, torch.bfloat16: MSDA_BF16}
     kinds = [set(map(dtype_of, grads)), set(map(dtype_of, outs))]

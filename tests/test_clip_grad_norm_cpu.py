@@ -46,3 +46,11 @@ def test_layouts_without_gaps_in_the_same_order():
     assert same(square.t(), square.t()) and not same(square, square.t())
     assert same(torch.empty(()), torch.empty(()))
     assert same(torch.empty(5, 0), torch.empty(5, 0)) and same(torch.empty(0, 5).t(), torch.empty(0, 5).t())
+
+
+@pytest.mark.parametrize("grads", [[None], [torch.ones(3), None], [3.0], [torch.ones(3)]])
+def test_what_is_no_cuda_tensor_is_refused(grads):
+    with pytest.raises(msda.MsdaError, match="msda_clip_grad_norm"):
+        msda.msda_clip_grad_norm(grads, 1.0)
+    with pytest.raises(msda.MsdaError, match="msda_clip_grad_norm"):
+        msda.msda_clip_grad_norm([], 1.0, total_norm=grads[-1])
