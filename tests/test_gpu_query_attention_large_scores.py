@@ -22,8 +22,8 @@ from tests import test_gpu_query_attention as attention
 
 pytestmark = pytest.mark.gpu
 
-# the last: two heads per CTA; the others: split keys, one tile, more queries than keys
-SIZES = [(1, 300, 200, 2), (2, 5, 700, 2), (1, 40, 9, 3), (4, 2400, 75, 8)]
+# split keys, one tile, more tiles than the visibility is looked up for at once, two heads per CTA
+SIZES = [(1, 300, 200, 2), (2, 5, 700, 2), (1, 40, 9, 3), (1, 70, 20_000, 1), (4, 2400, 75, 8)]
 
 
 def line(B, Nq, Nk, H, tau, groups, seed):
@@ -71,6 +71,41 @@ def test_a_tau_that_cuts_off_all_but_the_nearest(size, tau, groups):
     assert bool((gk.double().abs() <= sums[2]).all())
     assert bool((gt.double().abs() <= ds[..., 0]).all())
     assert bool(((gv.double() - sums[0]).abs() <= 2.0 ** -16 * sums[1] + 2.0 ** -8 * sums[0].abs()).all())
+
+
+@pytest.mark.parametrize("size", SIZES + [(1, 900, 900, 8)])
+@pytest.mark.parametrize("tau", [1e8, 1e10, 1e30])
+@pytest.mark.parametrize("groups", [False, True])
+def test_a_cut_off_with_the_own_key_at_distance_zero(size, tau, groups):
+    """The score of the own key is near zero, those of all others are far: with split keys only
+    some CTAs of a cluster end far.  Every other weight is 0, the own one 1 up to e = 40 u S +
+    2^-19 = 2^-16 (S = scale sum |q k| < 100), twice that and a rounding to bf16 in out."""
+    B, Nq, Nk, H = size
+    a, near = line(*size, tau, groups, 80 + sum(size))
+    a["q_points"][..., 0] = near
+    on = torch.ones(B, Nq, 1, 1, device="cuda", dtype=torch.float64)
+    if groups:
+        on[:, -1] = 0
+    out, lse = msda.msda_query_attention(**a)
+    at = near[:, :, None, None].expand(B, Nq, H, 32)
+    k, v = (torch.gather(a[n].double(), 1, at) for n in ("k", "v"))
+    want = v * on
+    assert bool(((out.double().view(B, Nq, H, 32) - want).abs() <= (2.0 ** -7 + 2.0 ** -15) * want.abs()).all())
+    score = 32 ** -0.5 * (a["q"].double() * k).sum(-1)
+    off = (lse.permute(0, 2, 1).double() - score).abs()[on[..., 0, 0] > 0]
+    assert bool((off <= 2.0 ** -16).all())
+    do = torch.randn(B, Nq, H * 32, device="cuda", generator=torch.Generator(device="cuda").manual_seed(6)).bfloat16()
+    gq, gk, gv, gt = msda.msda_query_attention_backward(**a, lse=lse, grad_out=do)
+    d = do.double().view(B, Nq, H, 32) * on
+    ds = 2.0 ** -14 * (d * v).abs().sum(-1, keepdim=True)   # p (dp - p dp), each p off by 2^-16
+    sums = torch.zeros(3, B, Nk, H, 32, device="cuda", dtype=torch.float64)
+    sums[0].scatter_add_(1, at, d)
+    sums[1].scatter_add_(1, at, d.abs())
+    sums[2].scatter_add_(1, at, ds * a["q"].double().abs())
+    assert bool((gq.double().abs() <= ds * k.abs()).all())
+    assert bool((gk.double().abs() <= sums[2]).all())
+    assert bool((gt == 0).all())   # the only pair with a weight has the distance 0
+    assert bool(((gv.double() - sums[0]).abs() <= (2.0 ** -8 + 2.0 ** -14) * sums[1] + 2.0 ** -8 * sums[0].abs()).all())
 
 
 @pytest.mark.parametrize("size", SIZES)
