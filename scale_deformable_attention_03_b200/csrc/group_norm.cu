@@ -29,8 +29,8 @@
 // that reaches, and written once.  Six cameras (185 k rows of 256, fp32 to bf16):
 // 85 us, 473 MB at 5.5 TB/s with next to nothing left in L2 for the second pass;
 // taking the cameras in twos, so that a pass fits, costs as much in the ends of
-// its launches as it saves.  The gradient of the same in fp32: 162 us, 946 MB at
-// 5.8 TB/s.
+// its launches as it saves.  The gradient of the same in fp32: 165 us, 946 MB at
+// 5.7 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

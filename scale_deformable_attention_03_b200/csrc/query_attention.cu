@@ -12,7 +12,7 @@
 // With 32 channels per head the products are not what binds: a score costs 64
 // multiply-adds, but also an exponential, and a square root per pair of points
 // and two heads, at 16 per clock and SM.  On the 100 x 100 grid with 8 heads (8e8
-// pairs, 580 us) the exponential unit is busy half of the time, shared memory and
+// pairs, 571 us) the exponential unit is busy half of the time, shared memory and
 // instruction issue as well, the matrix pipe a third of it: no one unit binds,
 // four warps per scheduler do not cover one another's latencies.
 #include <algorithm>
@@ -70,7 +70,7 @@ __device__ __forceinline__ void load_keys(ForwardSmem<HP>& sm, int stage, const 
 // it), and leaves fp32 as a power of 2 from scores of 1e9 on.  So a CTA that ends with a
 // reference past kFarLog2 is walked again (kFar), with the references taken off the scores
 // themselves, base being 0: a score equal to its reference has the weight 1 at any size.
-// Always so would take 600 us for the 100 x 100 grid instead of 579, with a branch in
+// Always so would take 600 us for the 100 x 100 grid instead of 571, with a branch in
 // this walk 642.
 template <int HP, bool kBias, bool kGroups, bool kExact, bool kFar>
 __device__ __forceinline__ void walk(ForwardSmem<HP>& sm, const Inputs& in,

@@ -519,10 +519,10 @@ constexpr int kSms = 148;
 // and shorter CTAs are faster).  The keys are split until the CTAs fill a wave,
 // down to two tiles per CTA, and of long rows where it evens out the last wave:
 // 628 CTAs in waves of 592 take two of them (704 us for the 100 x 100 grid),
-// quartered they take five a quarter as long (580 us).  With groups only the fill
+// quartered they take five a quarter as long (571 us).  With groups only the fill
 // counts: the tiles that a CTA needs are few and lie together, and parts of a row
-// without any still look them up (10 000 queries in seven documents one after the
-// other: 244 us, with even waves 398 us; in one shared group 783 against 636 us).
+// without any still look them up (10 000 queries in seven equal documents one after
+// the other: 267 us, with even waves 404 us; in one shared group 776 against 636 us).
 struct Plan {
     int heads, splits, split_tiles;
 };
@@ -532,8 +532,8 @@ struct Plan {
 // rounding on average; over thousands of rows that is what it is, among the few of a
 // decoding step a single one stands out.  Those leave most of the GPU idle, so
 // that the second product costs them least: one query over 4097 keys, 16 heads,
-// 14.3 us on the GPU instead of 13.5.  40 000 rows (5000 queries) are spared it: 195 us
-// instead of 171, and 488 instead of 403 for the gradient's second kernel.
+// 15.0 us on the GPU instead of 13.9.  40 000 rows (5000 queries) are spared it: 203 us
+// instead of 176, and 479 instead of 385 for the gradient's second kernel.
 constexpr int64_t kExactRows = 1024;
 inline bool exact_of(int64_t rows) { return rows <= kExactRows; }
 

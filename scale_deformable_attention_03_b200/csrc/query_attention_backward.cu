@@ -10,9 +10,9 @@
 // (not from the rounded output of the forward): ds is then exact where one key
 // takes all the weight, and dtau, an fp32 sum of it, keeps fp32's precision.
 //
-// Like the forward it is bound by no single unit (5000 queries, 8 heads: 155 us for
-// D, exponential unit 60 % busy; 403 us for the gradients, shared memory 58 %,
-// issue 48 %, exponentials 43 %, matrix pipe 37 %): an exponential and a square
+// Like the forward it is bound by no single unit (5000 queries, 8 heads: 152 us for
+// D, exponential unit 66 % busy; 386 us for the gradients, shared memory 69 %,
+// issue 55 %, exponentials 51 %, matrix pipe 44 %): an exponential and a square
 // root per pair in each of the three walks, and nine products for the five that a
 // single walk with atomics would take.
 #include <algorithm>
