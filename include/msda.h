@@ -659,7 +659,8 @@ typedef struct {
  * Scores may be of any size as long as both their terms, divided by scale, stay
  * in fp32's range: the key with a row's highest score has the weight 1 before
  * the division by their sum, so a tau of 1e10 cuts off all but the nearest key.
- * As every fp32 score, they are off by some 2^-24 of their terms.
+ * As every fp32 score, they are off by some 2^-24 of their terms.  Distances are
+ * roots of fp32 squares: of points less than 1e18 apart, and 0 below 1e-19.
  * The products are exact and accumulate in fp32, softmax and sums are fp32;
  * the weights are rounded to bf16 for their product with v (to 16 bits for up to
  * 1024 queries times heads times items).  q, k, v and out

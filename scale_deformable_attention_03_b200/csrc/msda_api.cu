@@ -201,7 +201,7 @@ ScaWorkspace sca_workspace_carve(void* base, int B, int Ncam, int Nq, int H, boo
 
 extern "C" {
 
-int32_t msda_version(void) { return 10300; }  // 1.3.0: group norm, query attention, gradient clipping
+int32_t msda_version(void) { return 10301; }  // 1.3.1: norm statistics of any data, scores of any size
 
 const char* msda_status_string(msda_status_t status)
 {

@@ -198,6 +198,43 @@ def test_products_that_leave_one_key(size, bias, big):
     assert all(bool(torch.isfinite(t).all()) for t in (gq, gk, gv) + ((gt,) if bias else ()))
 
 
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("size", [(2, 100, 32, 2), (1, 33, 3000, 1), (4, 2400, 75, 8)])
+@pytest.mark.parametrize("scale,one", [(1e-6, 2.0 ** 40), (1e6, 1.0), (1e6, 2.0 ** 70)])
+def test_the_smallest_and_largest_scale(size, bias, scale, one):
+    """q_i . k_j is `one` for one key and 0 for the others; with a bias the score is a million
+    times larger than that at most.  One weight is 1, the others are 0 (1e6 apart)."""
+    B, Nq, Nk, H = size
+    a = attention.problem(*size, bias, None, 11, joint=False)
+    a["q"].zero_()
+    a["k"].zero_()
+    i = torch.arange(Nq, device="cuda")
+    a["q"][:, i, :, i % 32] = one
+    j = torch.arange(32, device="cuda")
+    a["k"][:, (j * 7) % Nk, :, j] = 1.0
+    near = ((i % 32) * 7 % Nk).expand(B, Nq)
+    out, lse = msda.msda_query_attention(**a, scale=scale)
+    at = near[:, :, None, None].expand(B, Nq, H, 32)
+    v = torch.gather(a["v"], 1, at)
+    assert torch.equal(out.view(B, Nq, H, 32), v)
+    want = one * scale
+    if bias:
+        b = torch.arange(B, device="cuda")[:, None]
+        d = (a["q_points"].double() - a["k_points"].double()[b, near]).norm(dim=-1)
+        want = want - a["tau"].double() * d[..., None]
+    assert bool(((lse.permute(0, 2, 1).double() - want).abs() <= 2.0 ** -21 * one * scale).all())
+    do = torch.randn(B, Nq, H * 32, device="cuda", generator=torch.Generator(device="cuda").manual_seed(7)).bfloat16()
+    gq, gk, gv, gt = msda.msda_query_attention_backward(**a, lse=lse, grad_out=do, scale=scale)
+    d = do.double().view(B, Nq, H, 32)
+    ds = 2.0 ** -17 * (d * v.double()).abs().sum(-1, keepdim=True)
+    sums = torch.zeros(2, B, Nk, H, 32, device="cuda", dtype=torch.float64)
+    sums[0].scatter_add_(1, at, d)
+    sums[1].scatter_add_(1, at, d.abs())
+    assert bool(((gv.double() - sums[0]).abs() <= 2.0 ** -16 * sums[1] + 2.0 ** -8 * sums[0].abs()).all())
+    assert bool((gq.double().abs() <= scale * ds * 1.01).all())
+    assert gt is None or bool((gt.double().abs() <= 2 * ds[..., 0]).all())
+
+
 @pytest.mark.parametrize("Nk", [90, 900])
 def test_a_nan_in_a_live_query_is_not_hidden(Nk):
     a = attention.problem(1, 20, Nk, 2, True, None, 3, joint=False)
